@@ -139,7 +139,7 @@ inline WsLayout make_layout(const ft_moe_shape& s, int T) {
 }
 
 // device error codes written into ws err[0]
-enum : uint32_t { kDevErrNone = 0, kDevErrBadExpert = 1, kDevErrTimeout = 2, kDevErrShape = 3, kDevErrBounds = 4 };
+enum : uint32_t { kDevErrNone = 0, kDevErrBadExpert = 1, kDevErrTimeout = 2, kDevErrShape = 3, kDevErrBounds = 4, kDevErrOffsets = 5 };
 
 #ifndef FT_DEBUG_BOUNDS
 #define FT_DEBUG_BOUNDS 0

@@ -63,6 +63,8 @@ template <class T> inline T* ws_at(void* ws, size_t off) { return reinterpret_ca
 // host helpers of the C-ABI layer (api.cu)
 ft_status fail(ft_status s, const char* fmt, ...);
 ft_status check_shape(const ft_moe_shape* s);
+ft_status check_ws(const ft_moe_shape* s, int T, const void* ws, size_t ws_bytes, WsLayout* out);
+ft_status check_weights(const ft_moe_shape* s, const ft_moe_weights* w, bool need_contig);
 ft_status cuda_ok(cudaError_t e, const char* what);
 ft_status cuda_state();
 DecodeArgs decode_args(const ft_moe_shape* s, int T, const ft_moe_weights* w, const void* x, const WsLayout& L,
@@ -106,6 +108,15 @@ cudaError_t launch_combine(int T, int H, int k, int S, int R, const uint16_t* o,
                            const float* gw, uint16_t* y, cudaStream_t st);
 cudaError_t launch_combine_dependent(int T, int H, int k, int S, int R, const uint16_t* o, const int32_t* inv_pos,
                            const float* gw, uint16_t* y, cudaStream_t st);   // PDL-launched after a decode expert kernel
+// gradients (backward.cu); NULL d_o / d_w, wr, dw / db: that part is not asked for
+cudaError_t launch_combine_backward(int T, int H, int k, int S, int R, const uint16_t* dy, const uint16_t* o,
+                                    const int32_t* inv_pos, const float* gw, uint16_t* d_o, float* d_w, cudaStream_t st);
+cudaError_t launch_permute_backward(int T, int H, int k, int S, int E, int R, const uint16_t* dxs, const int32_t* inv_pos,
+                                    const int32_t* idx, const float* dl, const float* wr, uint16_t* dx, cudaStream_t st);
+cudaError_t launch_route_backward(int T, int H, int k, int E, const uint16_t* x, const int32_t* idx, const float* gw,
+                                  const float* dgw, const int32_t* offsets, const int32_t* sorted_flat, float* dlogits,
+                                  float* dw, float* db, float* part, cudaStream_t st);
+size_t route_backward_part_bytes(int T, int H, int k);   // partial sums at `part`
 cudaError_t launch_unit_rms(int T, int H, const uint16_t* in, uint16_t* out, float eps, cudaStream_t st);
 
 }  // namespace ftmoe

@@ -1,0 +1,548 @@
+// Grouped product of two MXFP4 operands on the block-scaled tensor cores.
+//
+//   out[r, n] = sum_k a[r, k] * w[g(r), n, k]        for the rows r of each group g
+//
+// with the optional SwiGLU epilogue of the experts' first projection: h = silu(gate) * up from the
+// fp32 accumulators, quantised to MXFP4 in the same pass (h never exists in bf16).
+//
+// tcgen05.mma.kind::mxf4.block_scale takes both operands as stored -- packed E2M1 codes, one E8M0
+// scale per 32 elements (scale_vec::2X) -- and accumulates in fp32: every product of two E2M1 values
+// and two powers of two is exact, so the only rounding before the epilogue is the accumulation's.
+//
+// "Weights as A": M = 128 weight rows, N = the group's rows rounded up to 16, so a group of five
+// rows costs an N = 16 MMA.  Tiles are (group, at most BN rows, 128 weight rows); a group of n rows
+// is cut into ceil(n / BN) nearly equal pieces.  The tile list is built by every CTA from the group
+// offsets (a block scan), so nothing but the offsets has to come from the caller.
+//   BN = 224: two accumulators of 224 columns and two sets of scale columns fill the 512 TMEM
+//             columns; 4 stages of 47 KB.
+//   BN = 32:  few rows per group (decode batches): 8 stages of 22 KB keep more weight bytes in flight.
+//
+// Roles of the persistent CTA: warp 0 TMA producer (codes of both operands, 256-deep K stages, 128-byte
+// swizzle); warp 1 TMEM allocator and MMA issuer; warps 2-5 read the row-major scale bytes and lay them
+// out as tcgen05.cp source atoms (32 x 16 bytes per 128 rows and 128-deep K step: byte 16 (row % 32) +
+// 4 (row / 32) + j = row's scale of the step's block j); warps 6-13 epilogue, two per TMEM lane quarter.
+// The MMA thread copies a stage's atoms into TMEM right before the stage's MMAs (copies and MMAs of one
+// thread complete in issue order).  Every wait is bounded.
+#include "gemm_common.cuh"
+#include "mx4.cuh"
+
+namespace ftmoe {
+
+constexpr int kPxThreads = 448;
+constexpr int kPxLoaders = 4;                // scale warps
+constexpr int kPxEpi = 8;                    // epilogue warps
+constexpr int kPxK = 256;                    // K per stage: 128 bytes of codes per row
+constexpr int kPxABytes = 128 * 128;
+constexpr int kPxGroups = kMaxExperts + 1;
+constexpr int kPxHRow = 65;                  // fp32 per token row of the h buffer: 64 + 1 against bank conflicts
+
+template <int BN>
+struct PxCfg {
+    static constexpr int kStages = BN == 32 ? 8 : 4;
+    static constexpr int kHalves = BN > 128 ? 2 : 1;               // 128-row scale atoms of B per 128-deep K step
+    static constexpr int kBBytes = BN * 128;
+    static constexpr int kSfA = 2 * 512;
+    static constexpr int kSfBytes = kSfA + 2 * kHalves * 512;
+    static constexpr int kSfCols = 2 * 4 + 2 * 4 * kHalves;        // TMEM columns of one stage's scales
+    static constexpr int kSfBase = 2 * BN;                         // after the two accumulators
+    static constexpr int kTmemCols = BN == 32 ? 128 : 512;
+    static constexpr int kEpiBytes = 2 * 32 * kPxHRow * 4;         // >= 8 x 2 KB transpose buffers
+    static constexpr size_t smem() {
+        return 1024 + size_t(kStages) * (kPxABytes + kBBytes + kSfBytes) + kEpiBytes + (3 * kStages + 8) * 8 +
+               (2 * (kPxGroups + 1) + 32) * 4;
+    }
+    static_assert(kSfBase + 2 * kSfCols <= kTmemCols, "TMEM columns");
+    static_assert(kEpiBytes >= kPxEpi * kXposeBytes, "epilogue buffers");
+};
+
+struct PxParams {
+    int K, nk, m_tiles, G, E, R;
+    int N;                    // bf16 output columns, or weight rows per group with SwiGLU (2F)
+    int vec;                  // bytes a scale load may take: 16, 8 or 2
+    const int32_t* offsets;
+    const uint8_t* wsc;
+    const uint8_t* swsc;
+    const uint8_t* asc;
+    uint16_t* out;
+    uint8_t* hq;
+    uint8_t* hs;
+    uint32_t* err;
+    unsigned long long wait_ns;
+};
+
+// kind::mxf4 instruction descriptor: E2M1 x E2M1, both K-major, E8M0 scales, M = 128; the scale
+// ids (0 or 2) select which two of a column word's four scale bytes the 64-deep MMA takes
+__device__ __forceinline__ uint32_t idesc_mxf4(int N, uint32_t sf_id) {
+    return (sf_id << 4) | (1u << 7) | (1u << 10) | (uint32_t(N >> 3) << 17) | (1u << 23) | (uint32_t(128 >> 4) << 24) |
+           (sf_id << 29);
+}
+__device__ __forceinline__ void umma_mxf4(uint32_t dtm, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t tsfa,
+                                          uint32_t tsfb, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+        ::"r"(dtm), "l"(ad), "l"(bd), "r"(idesc), "r"(acc), "r"(tsfa), "r"(tsfb));
+}
+// source descriptor of a scale atom (contiguous, no swizzle) and its copy to four TMEM columns,
+// repeated in every lane quarter
+__device__ __forceinline__ uint64_t px_atom_desc(uint32_t saddr) {
+    return uint64_t((saddr >> 4) & 0x3FFFu) | uint64_t(128 >> 4) << 16 | uint64_t(128 >> 4) << 32 | uint64_t(1) << 46;
+}
+__device__ __forceinline__ void px_copy_atom(uint32_t taddr, uint64_t d) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+__device__ __forceinline__ bool px_wait(uint64_t* b, uint32_t parity, volatile int* abort, unsigned long long limit) {
+    return mbar_try(b, parity) || mbar_wait(b, parity, abort, limit);
+}
+__device__ __forceinline__ bool px_warp_wait(uint64_t* b, uint32_t parity, volatile int* abort, unsigned long long limit) {
+    int r = 0;
+    if ((threadIdx.x & 31) == 0) r = px_wait(b, parity, abort, limit) ? 1 : 0;
+    r = __shfl_sync(0xffffffffu, r, 0);
+    __syncwarp();
+    return r != 0;
+}
+__device__ __forceinline__ void px_bar(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+
+struct PxTile { int g, m, row0, nvalid; };
+
+// tile t -> group, 128-row weight tile m (fastest, so CTAs that share rows of `a` run together), rows
+template <int BN>
+__device__ __forceinline__ PxTile px_tile(int t, const int* ntile, const int* off, int G, int m_tiles) {
+    PxTile r;
+    const int u = t / m_tiles;
+    r.m = t - u * m_tiles;
+    int lo = 0, hi = G;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (ntile[mid] <= u) lo = mid; else hi = mid;
+    }
+    r.g = lo;
+    const int n = off[lo + 1] - off[lo], nt = ntile[lo + 1] - ntile[lo];
+    const int per = ((n + nt - 1) / nt + 15) & ~15;     // <= BN, and (nt - 1) * per < n
+    const int i = u - ntile[lo];
+    r.row0 = off[lo] + i * per;
+    r.nvalid = min(per, n - i * per);
+    return r;
+}
+
+// 32 scale bytes (1024 elements) of a row from byte 32 c on; bytes past the row's nsc are 127 (2^0)
+__device__ __forceinline__ void px_load_scales(const uint8_t* row, int c, int nsc, int vec, bool valid, uint32_t (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0x7F7F7F7Fu;
+    if (!valid) return;
+    const int o = 32 * c;
+    if (vec == 16) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (o + 16 * i < nsc) {
+                const uint4 u = *reinterpret_cast<const uint4*>(row + o + 16 * i);
+                v[4 * i] = u.x; v[4 * i + 1] = u.y; v[4 * i + 2] = u.z; v[4 * i + 3] = u.w;
+            }
+    } else if (vec == 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (o + 8 * i < nsc) {
+                const uint2 u = *reinterpret_cast<const uint2*>(row + o + 8 * i);
+                v[2 * i] = u.x; v[2 * i + 1] = u.y;
+            }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t lo = 0x7F7Fu, hi = 0x7F7Fu;
+            if (o + 4 * i < nsc) lo = row[o + 4 * i] | uint32_t(row[o + 4 * i + 1]) << 8;
+            if (o + 4 * i + 2 < nsc) hi = row[o + 4 * i + 2] | uint32_t(row[o + 4 * i + 3]) << 8;
+            v[i] = lo | hi << 16;
+        }
+    }
+}
+
+template <bool SWIGLU, int BN>
+__global__ void __launch_bounds__(kPxThreads, 1)
+mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_sw,
+                   const __grid_constant__ CUtensorMap tm_a, PxParams p) {
+    using C = PxCfg<BN>;
+    constexpr int kSt = C::kStages;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sA = smem;
+    uint8_t* sB = sA + kSt * kPxABytes;
+    uint8_t* sSf = sB + kSt * C::kBBytes;
+    uint8_t* sEpi = sSf + kSt * C::kSfBytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + C::kEpiBytes);
+    uint64_t* sfull = full + kSt;
+    uint64_t* empty = sfull + kSt;
+    uint64_t* tfull = empty + kSt;
+    uint64_t* tempty = tfull + 2;
+    uint64_t* mma_done = tempty + 2;
+    int* ntile = reinterpret_cast<int*>(mma_done + 1);      // [G + 1] first row tile of each group
+    int* off = ntile + kPxGroups + 1;                       // [G + 1] row offsets
+    int* wsum = off + kPxGroups + 1;                        // block scan, then the epilogue's wait outcomes
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(wsum + 16);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* epi_ok = abort_flag + 1;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = p.G;
+    // ---- tile list: offsets clamped to [0, R] (a caller's bad table is reported, never followed)
+    int nt = 0;
+    if (tid < G) {
+        const int lo0 = p.offsets[tid], hi0 = p.offsets[tid + 1];
+        const int lo = min(max(lo0, 0), p.R), hi = min(max(hi0, lo), p.R);
+        if ((lo != lo0 || hi != hi0) && blockIdx.x == 0) atomicExch(p.err, kDevErrOffsets);
+        off[tid] = lo;
+        // a group's end is the next group's clamped start; the two only differ in a table already reported
+        nt = (max(min(max(hi0, 0), p.R) - lo, 0) + BN - 1) / BN;
+        if (tid == G - 1) off[G] = hi;
+    }
+    int inc = nt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += up;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    if (tid == 0) {
+        for (int s = 0; s < kSt; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&sfull[s], kPxLoaders);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull[b], 1);
+            mbar_init(&tempty[b], kPxEpi);
+        }
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        ntile[0] = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(tmem_slot)),
+                     "r"(C::kTmemCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    __syncthreads();
+    if (tid < G) {
+        for (int w = 0; w < warp; ++w) inc += wsum[w];
+        ntile[tid + 1] = inc;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int total = ntile[G] * p.m_tiles;
+    const int nk = p.nk;
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        if (lane == 0) {
+            int s = 0, step = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+                const PxTile tl = px_tile<BN>(t, ntile, off, G, p.m_tiles);
+                const bool shared_grp = tl.g >= p.E;
+                const CUtensorMap* mw = shared_grp ? &tm_sw : &tm_w;
+                const int wg = shared_grp ? 0 : tl.g;
+                const int nbox = (tl.nvalid + 31) >> 5;
+                const uint32_t bytes = uint32_t(kPxABytes) + uint32_t(nbox) * 4096u;
+                for (int kb = 0; kb < nk; ++kb, ++step) {
+                    if (!px_wait(&empty[s], phase ^ 1u, abort_flag, p.wait_ns)) { ok = false; break; }
+                    mbar_expect_tx(&full[s], bytes);
+                    uint8_t* a = sA + s * kPxABytes;
+                    if (SWIGLU) tma_5d(mw, &full[s], a, kb * 128, 0, 0, tl.m * 4, wg);
+                    else tma_3d(mw, &full[s], a, kb * 128, tl.m * 128, wg);
+                    for (int b = 0; b < nbox; ++b)
+                        tma_2d(&tm_a, &full[s], sB + s * C::kBBytes + b * 4096, kb * 128, tl.row0 + 32 * b);
+                    if (++s == kSt) { s = 0; phase ^= 1u; }
+                }
+            }
+            if (!ok) { *abort_flag = 1; atomicExch(p.err, kDevErrTimeout); }
+            for (int st = step > kSt ? step - kSt : 0; st < step; ++st)     // own copies in flight have landed
+                mbar_wait(&full[st % kSt], uint32_t(st / kSt) & 1u, nullptr);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ scale copies and MMAs, one thread
+        if (lane == 0) {
+            const uint64_t ad0 = sdesc_sw128(su32(sA)), bd0 = sdesc_sw128(su32(sB));
+            const uint64_t sf0 = px_atom_desc(su32(sSf));
+            int s = 0, j = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++j) {
+                const PxTile tl = px_tile<BN>(t, ntile, off, G, p.m_tiles);
+                const int N = (tl.nvalid + 15) & ~15;
+                const int buf = j & 1;
+                if (!px_wait(&tempty[buf], (uint32_t(j >> 1) & 1u) ^ 1u, abort_flag, p.wait_ns)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t dacc = tmem + uint32_t(BN * buf);
+                const uint32_t id0 = idesc_mxf4(N, 0), id2 = idesc_mxf4(N, 2);
+                const bool two = C::kHalves == 2 && N > 128;
+                for (int kb = 0; kb < nk; ++kb) {
+                    if (!px_wait(&full[s], phase, abort_flag, p.wait_ns) ||
+                        !px_wait(&sfull[s], phase, abort_flag, p.wait_ns)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t sfa = tmem + uint32_t(C::kSfBase + (s & 1) * C::kSfCols), sfb = sfa + 8u;
+                    const uint64_t sd = sf0 + uint64_t((s * C::kSfBytes) >> 4);
+#pragma unroll
+                    for (int a = 0; a < 2; ++a) {
+                        px_copy_atom(sfa + 4u * a, sd + uint64_t(32 * a));
+                        px_copy_atom(sfb + 4u * C::kHalves * a, sd + uint64_t((C::kSfA + a * C::kHalves * 512) >> 4));
+                        if (two) px_copy_atom(sfb + 4u * C::kHalves * a + 4u, sd + uint64_t((C::kSfA + a * C::kHalves * 512 + 512) >> 4));
+                    }
+                    const uint64_t ad = ad0 + uint64_t((s * kPxABytes) >> 4), bd = bd0 + uint64_t((s * C::kBBytes) >> 4);
+                    const int steps = min(4, (p.K - kb * kPxK) >> 6);       // 64-deep MMAs of this stage
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (i >= steps) break;
+                        const uint32_t hi = (i & 1) ? 2u << 30 : 0u;
+                        umma_mxf4(dacc, ad + uint64_t(2 * i), bd + uint64_t(2 * i), (i & 1) ? id2 : id0,
+                                  (sfa + 4u * (i >> 1)) | hi, (sfb + 4u * C::kHalves * (i >> 1)) | hi, (kb | i) != 0);
+                    }
+                    umma_commit(&empty[s]);
+                    if (++s == kSt) { s = 0; phase ^= 1u; }
+                }
+                if (!ok) break;
+                umma_commit(&tfull[buf]);
+            }
+            if (!ok) { *abort_flag = 1; atomicExch(p.err, kDevErrTimeout); }
+            umma_commit(mma_done);
+            mbar_wait(mma_done, 0, nullptr);
+        }
+    } else if (warp < 2 + kPxLoaders) {
+        // ------------------------------------------------ scale bytes -> atoms, four stages per load
+        // Thread i takes A row i and B rows i, i + 128; the next 32 bytes of each are in flight while
+        // the current ones are laid out.
+        const int i = tid - 64;
+        const int nsc = p.K / 32, nch = (nk + 3) >> 2;
+        const int at = 16 * (i & 31) + 4 * (i >> 5);
+        uint32_t cur[1 + C::kHalves][8], nxt[1 + C::kHalves][8];
+        auto load = [&](int t, int c, uint32_t (&v)[1 + C::kHalves][8]) {
+            const PxTile tl = px_tile<BN>(t, ntile, off, G, p.m_tiles);
+            const bool shared_grp = tl.g >= p.E;
+            int wrow;
+            if (SWIGLU) {
+                const int F = p.N >> 1, f = tl.m * 64 + 16 * (i >> 5) + (i & 15);
+                wrow = (i & 31) < 16 ? f : F + f;
+            } else {
+                wrow = tl.m * 128 + i;
+            }
+            const uint8_t* wr = (shared_grp ? p.swsc : p.wsc) + (size_t(shared_grp ? 0 : tl.g) * p.N + wrow) * nsc;
+            px_load_scales(wr, c, nsc, p.vec, wrow < p.N, v[0]);
+#pragma unroll
+            for (int h = 0; h < C::kHalves; ++h) {
+                const int r = i + 128 * h;
+                px_load_scales(p.asc + size_t(tl.row0 + r) * nsc, c, nsc, p.vec, r < tl.nvalid, v[1 + h]);
+            }
+        };
+        int s = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        int t = blockIdx.x, c = 0;
+        if (t < total) load(t, 0, cur);
+        while (t < total && ok) {
+            int tn = t, cn = c + 1;
+            if (cn == nch) { cn = 0; tn += gridDim.x; }
+            if (tn < total) load(tn, cn, nxt);
+#pragma unroll
+            for (int sub = 0; sub < 4; ++sub) {
+                if (4 * c + sub >= nk || !ok) break;
+                if (!px_warp_wait(&empty[s], phase ^ 1u, abort_flag, p.wait_ns)) { ok = false; break; }
+                uint8_t* d = sSf + s * C::kSfBytes + at;
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    *reinterpret_cast<uint32_t*>(d + 512 * a) = cur[0][2 * sub + a];
+#pragma unroll
+                    for (int h = 0; h < C::kHalves; ++h)
+                        *reinterpret_cast<uint32_t*>(d + C::kSfA + (a * C::kHalves + h) * 512) = cur[1 + h][2 * sub + a];
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sfull[s]);
+                if (++s == kSt) { s = 0; phase ^= 1u; }
+            }
+            t = tn;
+            c = cn;
+#pragma unroll
+            for (int h = 0; h < 1 + C::kHalves; ++h)
+#pragma unroll
+                for (int x = 0; x < 8; ++x) cur[h][x] = nxt[h][x];
+        }
+        if (!ok) { *abort_flag = 1; if (lane == 0) atomicExch(p.err, kDevErrTimeout); }
+    } else {
+        // ------------------------------------------------ epilogue
+        const int q = warp & 3;                       // TMEM lanes 32q .. 32q + 31
+        const int half = (warp - 2 - kPxLoaders) >> 2;   // column chunks half, half + 2, ...
+        const int et = tid - 32 * (2 + kPxLoaders) - 128 * half;   // 0..127 within the half
+        const bool lead = warp == 2 + kPxLoaders + 4 * half;
+        bool ok = true;
+        int j = 0;
+        for (int t = blockIdx.x; t < total; t += gridDim.x, ++j) {
+            const PxTile tl = px_tile<BN>(t, ntile, off, G, p.m_tiles);
+            const int buf = j & 1;
+            const uint32_t par = uint32_t(j >> 1) & 1u;
+            if (SWIGLU) {
+                // the half's four warps meet at barriers below, so they take one common outcome
+                if (lead) {
+                    const bool r = px_warp_wait(&tfull[buf], par, abort_flag, p.wait_ns);
+                    if (lane == 0) epi_ok[half] = r;
+                    __threadfence_block();
+                }
+                px_bar(1 + half);
+                ok = epi_ok[half] != 0;
+                px_bar(1 + half);
+            } else {
+                ok = px_warp_wait(&tfull[buf], par, abort_flag, p.wait_ns);
+            }
+            if (!ok) break;
+            tc_fence_after();
+            const int nch = (tl.nvalid + 31) >> 5;
+            const uint32_t tb = tmem + (uint32_t(q * 32) << 16) + uint32_t(BN * buf);
+            for (int c = half; c < nch; c += 2) {
+                float v[32];
+                tmem_ld32_nowait(tb + uint32_t(32 * c), v);
+                tmem_wait_16(v);
+                tmem_fence_regs(v + 16);
+                if (c + 2 >= nch) {                    // this warp's last read of the accumulator
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&tempty[buf]);
+                }
+                if constexpr (SWIGLU) {
+                    // lanes 0-15 hold gate rows f, lanes 16-31 the matching up rows: halves swap so that
+                    // each lane finishes 16 tokens of its f, staged as fp32 [token][64 f]
+                    float* hb = reinterpret_cast<float*>(sEpi) + half * 32 * kPxHRow;
+                    const int fl = 16 * q + (lane & 15);
+                    const bool lo = lane < 16;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float send = lo ? v[16 + i] : v[i];
+                        const float recv = __shfl_xor_sync(0xffffffffu, send, 16);
+                        const float gt = lo ? v[i] : recv;
+                        const float up = lo ? recv : v[16 + i];
+                        // expf, not the tanh approximation of the bf16 paths: the E2M1 rounding that
+                        // follows turns an error near a rounding border into a whole step
+                        hb[(lo ? i : 16 + i) * kPxHRow + fl] = gt / (1.f + expf(-gt)) * up;
+                    }
+                    px_bar(1 + half);
+                    const int tok = et >> 2, part = et & 3;   // two threads per 32-element block
+                    const float* hr = hb + tok * kPxHRow + 16 * part;
+                    float x[16];
+                    uint32_t m = 0;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) { x[i] = hr[i]; m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu); }
+                    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                    float mul;
+                    const uint32_t sc = mx4_scale_of(m, mul);
+                    float y[8], z[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) { y[i] = x[i] * mul; z[i] = x[8 + i] * mul; }
+                    uint2 cd = make_uint2(e2m1x8(y), e2m1x8(z));
+                    if (sc == 255u) cd = make_uint2(0u, 0u);
+                    const int n = 32 * c + tok;
+                    if (n < tl.nvalid) {
+                        const int F = p.N >> 1;
+                        const size_t row = size_t(tl.row0 + n);
+                        *reinterpret_cast<uint2*>(p.hq + row * (F >> 1) + tl.m * 32 + 8 * part) = cd;
+                        if (!(part & 1)) p.hs[row * (F >> 5) + tl.m * 2 + (part >> 1)] = uint8_t(sc);
+                    }
+                    px_bar(1 + half);
+                } else {
+                    uint16_t* xb = reinterpret_cast<uint16_t*>(sEpi + (warp - 2 - kPxLoaders) * kXposeBytes);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) xb[i * 32 + lane] = f2bf(v[i]);
+                    __syncwarp();
+                    const int col = tl.m * 128 + 32 * q;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int ch = lane + 32 * r, tok = ch >> 2, pp = ch & 3;
+                        const int n = 32 * c + tok;
+                        if (n < tl.nvalid && col + 8 * pp < p.N)
+                            *reinterpret_cast<uint4*>(p.out + size_t(tl.row0 + n) * p.N + col + 8 * pp) =
+                                *reinterpret_cast<const uint4*>(xb + tok * 32 + 8 * pp);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (half >= nch) {                         // no chunk of this tile is this warp's
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tempty[buf]);
+            }
+        }
+        if (!ok) { *abort_flag = 1; if (lane == 0) atomicExch(p.err, kDevErrTimeout); }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols));
+    }
+}
+
+template <bool SWIGLU, int BN>
+static int launch_variant(int grid, cudaStream_t st, const CUtensorMap& tw, const CUtensorMap& tsw, const CUtensorMap& ta,
+                          const PxParams& p) {
+    constexpr size_t smem = PxCfg<BN>::smem();
+    static PerDeviceOnce attr;
+    if (attr([&] {
+            return cudaFuncSetAttribute(mx4_product_kernel<SWIGLU, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        }) != cudaSuccess)
+        return 2;
+    mx4_product_kernel<SWIGLU, BN><<<grid, kPxThreads, smem, st>>>(tw, tsw, ta, p);
+    return cudaGetLastError() == cudaSuccess ? 0 : 2;
+}
+
+int launch_mx4_product(const Mx4Launch& L, cudaStream_t st) {
+    const int wrows = L.swiglu ? 2 * L.N : L.N;        // weight rows per group
+    const uint64_t kb = uint64_t(L.K) / 2;             // code bytes per row
+    CUtensorMap tw{}, tsw{}, ta{};
+    {
+        uint64_t dims[2] = {kb, uint64_t(L.R)};
+        uint64_t str[1] = {kb};
+        uint32_t box[2] = {128, 32};
+        if (!make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, L.a, 2, dims, str, box)) return 1;
+    }
+    auto weight_map = [&](CUtensorMap* m, const uint8_t* w, int groups) {
+        if (L.swiglu) {
+            // [E][2][F][K/2] viewed as (K/2, 16, 2, F/16, E): a box of four blocks of 16 gate rows, each
+            // followed by the 16 matching up rows
+            const uint64_t F = uint64_t(L.N);
+            uint64_t dims[5] = {kb, 16, 2, F / 16, uint64_t(groups)};
+            uint64_t str[4] = {kb, F * kb, 16 * kb, 2 * F * kb};
+            uint32_t box[5] = {128, 16, 2, 4, 1};
+            return make_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, 5, dims, str, box);
+        }
+        uint64_t dims[3] = {kb, uint64_t(L.N), uint64_t(groups)};
+        uint64_t str[2] = {kb, uint64_t(L.N) * kb};
+        uint32_t box[3] = {128, 128, 1};
+        return make_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, 3, dims, str, box);
+    };
+    if (!weight_map(&tw, L.w, L.E)) return 1;
+    if (L.G > L.E) {
+        if (!weight_map(&tsw, L.sw, 1)) return 1;
+    } else {
+        tsw = tw;
+    }
+    PxParams p{};
+    p.K = L.K;
+    p.nk = (L.K + kPxK - 1) / kPxK;
+    p.m_tiles = L.swiglu ? L.N / 64 : (L.N + 127) / 128;
+    p.G = L.G; p.E = L.E; p.R = L.R; p.N = wrows;
+    p.offsets = L.offsets;
+    p.wsc = L.ws; p.swsc = L.sws; p.asc = L.as;
+    p.out = L.out; p.hq = L.hq; p.hs = L.hs;
+    p.err = L.err;
+    p.wait_ns = gemm_wait_ns();
+    const uintptr_t al = reinterpret_cast<uintptr_t>(L.ws) | reinterpret_cast<uintptr_t>(L.as) |
+                         (L.G > L.E ? reinterpret_cast<uintptr_t>(L.sws) : 0) | uintptr_t(L.K / 32);
+    p.vec = al % 16 == 0 ? 16 : al % 8 == 0 ? 8 : 2;
+    const bool small = L.R <= 16 * L.G;
+    const int64_t bn = small ? 32 : 224;
+    const int64_t tiles = int64_t(p.m_tiles) * (int64_t(L.G < L.R ? L.G : L.R) + L.R / bn);   // an upper bound
+    const int grid = int(tiles < num_sms() ? tiles : num_sms());
+    if (L.swiglu) return small ? launch_variant<true, 32>(grid, st, tw, tsw, ta, p) : launch_variant<true, 224>(grid, st, tw, tsw, ta, p);
+    return small ? launch_variant<false, 32>(grid, st, tw, tsw, ta, p) : launch_variant<false, 224>(grid, st, tw, tsw, ta, p);
+}
+
+}  // namespace ftmoe

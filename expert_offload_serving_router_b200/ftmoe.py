@@ -22,6 +22,7 @@ HEADER = os.path.join(os.path.dirname(PKG), "include", "ftmoe.h")
 FT_OK, FT_ERR_INVALID_ARG, FT_ERR_UNSUPPORTED, FT_ERR_CUDA, FT_ERR_WORKSPACE, FT_ERR_NOT_PINNED, \
     FT_ERR_TIMEOUT, FT_ERR_DEVICE_CHECK = range(8)
 FT_W_BF16, FT_W_MXFP4 = 0, 1
+FT_T_BF16, FT_T_FP16, FT_T_FP32 = 0, 1, 2
 FT_CACHE_PER_LAYER, FT_CACHE_GLOBAL = 0, 1
 
 c_i32, c_i64, c_u64, c_sz, c_vp, c_f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_size_t, \
@@ -77,6 +78,17 @@ _SIGS = {
     "ft_moe_combine": (c_i32, [ctypes.POINTER(ft_moe_shape), c_i32, c_vp, c_vp, c_vp, c_vp, c_vp]),
     "ft_moe_layer_forward": (c_i32, [ctypes.POINTER(ft_moe_shape), c_i32, c_vp, c_vp, c_vp, ctypes.POINTER(ft_moe_weights),
                                      c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "ft_mx4_quantize": (c_i32, [c_i64, c_i32, c_i32, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp]),
+    "ft_mx4_product_workspace_bytes": (c_sz, [c_i32, c_i32, c_i32, c_i32]),
+    "ft_mx4_product": (c_i32, [c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "ft_moe_experts_mx4": (c_i32, [ctypes.POINTER(ft_moe_shape), c_i32, ctypes.POINTER(ft_moe_weights), c_vp, c_vp, c_vp,
+                                   c_vp, c_vp, c_sz, c_vp]),
+    "ft_moe_layer_forward_mx4": (c_i32, [ctypes.POINTER(ft_moe_shape), c_i32, c_vp, c_vp, c_vp,
+                                         ctypes.POINTER(ft_moe_weights), c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "ft_moe_combine_backward": (c_i32, [ctypes.POINTER(ft_moe_shape), c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "ft_moe_permute_backward": (c_i32, [ctypes.POINTER(ft_moe_shape), c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "ft_moe_route_backward": (c_i32, [ctypes.POINTER(ft_moe_shape), c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                      c_vp, c_vp, c_sz, c_vp]),
     "ft_moe_unit_rms": (c_i32, [c_i32, c_i32, c_vp, c_vp, c_f32, c_vp]),
     "ft_expert_stream_arena_bytes": (c_sz, [ctypes.POINTER(ft_stream_cfg)]),
     "ft_expert_stream_create": (c_i32, [ctypes.POINTER(ft_stream_cfg), ctypes.POINTER(c_vp)]),
@@ -251,6 +263,48 @@ def ft_moe_layer_forward(shape, T, x, w_router, bias, weights, y, topk_idx_out, 
 
 def ft_moe_unit_rms(T, H, x_in, x_out, eps=1e-6, stream=None):
     _check(lib().ft_moe_unit_rms(T, H, _p(x_in), _p(x_out), eps, _s(stream)))
+
+
+def ft_mx4_quantize(rows, cols, dtype, x, x_stride, codes, scales, values=None, stream=None):
+    _check(lib().ft_mx4_quantize(rows, cols, dtype, _p(x), x_stride, _p(codes), _p(scales), _p(values), _s(stream)))
+
+
+def ft_mx4_product_workspace_bytes(groups, rows, n, k) -> int:
+    return lib().ft_mx4_product_workspace_bytes(groups, rows, n, k)
+
+
+def ft_mx4_product(groups, rows, n, k, offsets, a_codes, a_scales, w_codes, w_scales, out, ws, ws_bytes=None, stream=None):
+    _check(lib().ft_mx4_product(groups, rows, n, k, _p(offsets), _p(a_codes), _p(a_scales), _p(w_codes), _p(w_scales),
+                                _p(out), _p(ws), _nbytes(ws, ws_bytes), _s(stream)))
+
+
+def ft_moe_experts_mx4(shape, T, weights, x, offsets, inv_pos, o_sorted, ws, ws_bytes=None, stream=None):
+    _check(lib().ft_moe_experts_mx4(ctypes.byref(shape), T, ctypes.byref(weights), _p(x), _p(offsets), _p(inv_pos),
+                                    _p(o_sorted), _p(ws), _nbytes(ws, ws_bytes), _s(stream)))
+
+
+def ft_moe_layer_forward_mx4(shape, T, x, w_router, bias, weights, y, topk_idx_out, logits_out, ws, ws_bytes=None,
+                             stream=None):
+    _check(lib().ft_moe_layer_forward_mx4(ctypes.byref(shape), T, _p(x), _p(w_router), _p(bias), ctypes.byref(weights),
+                                          _p(y), _p(topk_idx_out), _p(logits_out), _p(ws), _nbytes(ws, ws_bytes),
+                                          _s(stream)))
+
+
+def ft_moe_combine_backward(shape, T, dy, o_sorted, inv_pos, topk_w, d_o_sorted, d_topk_w, stream=None):
+    _check(lib().ft_moe_combine_backward(ctypes.byref(shape), T, _p(dy), _p(o_sorted), _p(inv_pos), _p(topk_w),
+                                         _p(d_o_sorted), _p(d_topk_w), _s(stream)))
+
+
+def ft_moe_permute_backward(shape, T, dx_sorted, inv_pos, topk_idx, dlogits, w_router, dx, stream=None):
+    _check(lib().ft_moe_permute_backward(ctypes.byref(shape), T, _p(dx_sorted), _p(inv_pos), _p(topk_idx), _p(dlogits),
+                                         _p(w_router), _p(dx), _s(stream)))
+
+
+def ft_moe_route_backward(shape, T, x, topk_idx, topk_w, d_topk_w, offsets, sorted_flat, dlogits, dw_router, dbias, ws,
+                          ws_bytes=None, stream=None):
+    _check(lib().ft_moe_route_backward(ctypes.byref(shape), T, _p(x), _p(topk_idx), _p(topk_w), _p(d_topk_w), _p(offsets),
+                                       _p(sorted_flat), _p(dlogits), _p(dw_router), _p(dbias), _p(ws),
+                                       _nbytes(ws, ws_bytes), _s(stream)))
 
 
 def ft_lru_step(E, n_slots, content, stamp, where, step, ids, out_slot, out_hit):

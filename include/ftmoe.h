@@ -91,6 +91,9 @@ typedef enum {
 
 typedef enum { FT_W_BF16 = 0, FT_W_MXFP4 = 1 } ft_wdtype;
 
+/* element types of ft_mx4_quantize's input */
+typedef enum { FT_T_BF16 = 0, FT_T_FP16 = 1, FT_T_FP32 = 2 } ft_dtype;
+
 typedef struct {
     int32_t hidden;       /* H */
     int32_t ffn;          /* F (per-expert SwiGLU width) */
@@ -272,6 +275,102 @@ ft_status ft_moe_layer_forward(const ft_moe_shape* shape, int32_t T, const void*
 /* Chaining helper for stacked layers: out[t,:] = bf16(in[t,:] / sqrt(mean_h
  * in[t,h]^2 + eps)), computed in fp32.  in, out: device [T,H] bf16 (may alias). */
 ft_status ft_moe_unit_rms(int32_t T, int32_t H, const void* in, void* out, float eps, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * MXFP4 quantisation, and products whose activations are MXFP4 too.
+ * Format: OCP Microscaling v1.0 as above.  Per block of 32 consecutive elements with
+ * m = max|v|: scale 2^e, e = max(floor(log2 m) - 2, -127) (2^0 for a block of zeros), scale
+ * byte e + 127; code = v * 2^-e rounded to nearest even on the E2M1 grid, saturated at 6, the
+ * sign kept (-0 too).  A block that holds a NaN or an infinity gets scale byte 0xFF and zero
+ * codes: all its values read as NaN, and so does every product with it.
+ * In products, the codes and scales are multiplied exactly (tcgen05 kind::mxf4, block-scaled)
+ * and summed in fp32.  Carrying the activations in 4 bits costs accuracy that the bf16
+ * paths keep (each activation is within 2^-2 of its value relative to the block's largest
+ * element's power of two); which form a layer runs is the caller's choice of entry point.
+ * ------------------------------------------------------------------------- */
+
+/* Quantises rows.  x: device [rows, cols] of `dtype` (ft_dtype) with x_stride elements from one
+ * row to the next (>= cols), aligned to its elements (16-byte aligned rows load fastest);
+ * cols % 32 == 0.  codes: device output [rows, cols/2], scales: device output [rows, cols/32] --
+ * the layout of the layer's MXFP4 weights, so a [E * 2F, H] weight matrix becomes w13 and
+ * w13_scale in one call.  values: optional device output [rows, cols] of `dtype`: the numbers
+ * the codes stand for (exact in bf16 and fp32; rounded in fp16 only below 2^-24), for
+ * quantisation-aware training and for checks; it must not overlap x.  codes and values:
+ * 16-byte aligned.  rows == 0 launches nothing. */
+ft_status ft_mx4_quantize(int64_t rows, int32_t cols, int32_t dtype, const void* x, int64_t x_stride, uint8_t* codes,
+                          uint8_t* scales, void* values, void* stream);
+
+/* Bytes of workspace ft_mx4_product needs (0 on invalid sizes). */
+size_t ft_mx4_product_workspace_bytes(int32_t groups, int32_t rows, int32_t n, int32_t k);
+
+/* Grouped product: out[r, :] = bf16(sum_k a[r, k] * w[g, :, k]) for the rows r in
+ * [offsets[g], offsets[g+1]) of each group g (groups == 1: one plain product).
+ * a: device codes [rows, k/2] + scales [rows, k/32]; w: device codes [groups, n, k/2] + scales
+ * [groups, n, k/32]; out: device [rows, n] bf16.  offsets: device [groups + 1] int32, ascending in
+ * [0, rows]; rows outside every group are not written.  A table that is not ascending or leaves
+ * [0, rows] is clamped (no access is out of range), the outputs are undefined and
+ * ft_moe_check(ws) returns FT_ERR_DEVICE_CHECK.
+ * groups <= 256, k % 64 == 0, k <= 16384, n % 8 == 0.  Codes and out 16-byte aligned, scales
+ * 2-byte aligned (16-byte aligned scale rows load fastest).  ws: device workspace of
+ * ft_mx4_product_workspace_bytes(...) bytes or more, prepared once by ft_moe_workspace_init;
+ * calls that may overlap need a workspace each. */
+ft_status ft_mx4_product(int32_t groups, int32_t rows, int32_t n, int32_t k, const int32_t* offsets, const uint8_t* a_codes,
+                         const uint8_t* a_scales, const uint8_t* w_codes, const uint8_t* w_scales, void* out, void* ws,
+                         size_t ws_bytes, void* stream);
+
+/* Step 3 on MXFP4 activations (MXFP4 weights, contiguous; any T): each token's row is quantised
+ * and put into its k (+ S) sorted places, h = silu(Wg xq) * (Wu xq) is quantised from fp32,
+ * o_sorted[r,:] = bf16(Wd hq).  x: device [T,H] bf16; offsets, inv_pos: as written by
+ * ft_moe_permute (its x_sorted is not needed: pass NULL there); o_sorted: device output [R,H].
+ * ws: scratch of ft_moe_workspace_bytes(shape, T) bytes or more. */
+ft_status ft_moe_experts_mx4(const ft_moe_shape* shape, int32_t T, const ft_moe_weights* weights, const void* x,
+                             const int32_t* offsets, const int32_t* inv_pos, void* o_sorted, void* ws, size_t ws_bytes,
+                             void* stream);
+
+/* ft_moe_layer_forward with step 3 on MXFP4 activations: same arguments, routing and combine. */
+ft_status ft_moe_layer_forward_mx4(const ft_moe_shape* shape, int32_t T, const void* x, const float* w_router,
+                                   const float* bias, const ft_moe_weights* weights, void* y, int32_t* topk_idx_out,
+                                   float* logits_out, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Gradients of steps 1, 2 and 4 (the experts' own gradient is the caller's).  Fixed-order fp32
+ * sums, no atomics: the same inputs give the same bits.  inv_pos, offsets, sorted_flat: as
+ * written by ft_moe_permute for topk_idx; a position outside [0,R) is a dropped pair (it
+ * contributes nothing), and after a batch that ft_moe_check reported the results are undefined
+ * but nothing out of range is touched.  T * (k + S) must fit in 31 bits.  Outputs must not
+ * overlap inputs.
+ * ------------------------------------------------------------------------- */
+
+/* Gradient of step 4.  dy: device [T,H] bf16, the gradient of y.
+ * d_o_sorted: device output [R,H] bf16, d_o_sorted[inv_pos[t*k+j]] = bf16(topk_w[t,j] * dy[t]) and
+ *   the shared row = dy[t]; NULL when the experts need no gradient.
+ * d_topk_w: device output [T,k] fp32, d_topk_w[t,j] = <o_sorted[inv_pos[t*k+j]], dy[t]>; NULL when
+ *   the gates need none (o_sorted may then be NULL too). */
+ft_status ft_moe_combine_backward(const ft_moe_shape* shape, int32_t T, const void* dy, const void* o_sorted,
+                                  const int32_t* inv_pos, const float* topk_w, void* d_o_sorted, float* d_topk_w,
+                                  void* stream);
+
+/* Gradient of step 2's gather, with the router's part of dx in the same pass: dx[t] = bf16(
+ * sum_j dx_sorted[inv_pos[t*k+j]] (+ dx_sorted[inv_pos[T*k+t]] when S = 1)
+ * (+ sum_j dlogits[t,j] * w_router[topk_idx[t,j]])), summed in fp32 and rounded once.
+ * dx_sorted: device [R,H] bf16; dx: device output [T,H] bf16; topk_idx [T,k], dlogits [T,k] fp32
+ * (from ft_moe_route_backward), w_router [E,H] fp32: device, all three or none. */
+ft_status ft_moe_permute_backward(const ft_moe_shape* shape, int32_t T, const void* dx_sorted, const int32_t* inv_pos,
+                                  const int32_t* topk_idx, const float* dlogits, const float* w_router, void* dx,
+                                  void* stream);
+
+/* Gradient of step 1 from the gradient of the gates (softmax over the kept logits; the other
+ * logits' gradient is zero): dlogits[t,j] = g_j (d_g_j - sum_i g_i d_g_i), device output [T,k]
+ * fp32, required.  dw_router: optional device output [E,H] fp32, sum over the pairs routed to e
+ * of dlogits * x[t]; dbias: optional device output [E] fp32 (both overwritten; zero for an expert
+ * without tokens, and for T = 0).  x: device [T,H] bf16 (needed for dw_router); topk_idx, offsets,
+ * sorted_flat (needed for dw_router or dbias); topk_w, d_topk_w: device [T,k] fp32.
+ * ws: scratch of ft_moe_workspace_bytes(shape, T) bytes or more (its row regions are
+ * overwritten). */
+ft_status ft_moe_route_backward(const ft_moe_shape* shape, int32_t T, const void* x, const int32_t* topk_idx,
+                                const float* topk_w, const float* d_topk_w, const int32_t* offsets,
+                                const int32_t* sorted_flat, float* dlogits, float* dw_router, float* dbias, void* ws,
+                                size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Host-resident experts: ft_expert_stream.
