@@ -41,6 +41,7 @@ struct PxCfg {
     static constexpr int kStages = BN == 32 ? 8 : 4;
     static constexpr int kHalves = BN > 128 ? 2 : 1;               // 128-row scale atoms of B per 128-deep K step
     static constexpr int kBBytes = BN * 128;
+    static constexpr int kBox = BN == 32 ? 16 : 32;                // rows of the smallest activation box; the others are 2x, 4x
     static constexpr int kSfA = 2 * 512;
     static constexpr int kSfBytes = kSfA + 2 * kHalves * 512;
     static constexpr int kSfCols = 2 * 4 + 2 * 4 * kHalves;        // TMEM columns of one stage's scales
@@ -48,7 +49,7 @@ struct PxCfg {
     static constexpr int kTmemCols = BN == 32 ? 128 : 512;
     static constexpr int kEpiBytes = 2 * 32 * kPxHRow * 4;         // >= 8 x 2 KB transpose buffers
     static constexpr size_t smem() {
-        return 1024 + size_t(kStages) * (kPxABytes + kBBytes + kSfBytes) + kEpiBytes + (3 * kStages + 8) * 8 +
+        return 1024 + size_t(kStages) * (kPxABytes + kBBytes + kSfBytes) + kEpiBytes + (2 * kStages + 8) * 8 +
                (2 * (kPxGroups + 1) + 32) * 4;
     }
     static_assert(kSfBase + 2 * kSfCols <= kTmemCols, "TMEM columns");
@@ -101,6 +102,15 @@ __device__ __forceinline__ bool px_warp_wait(uint64_t* b, uint32_t parity, volat
     __syncwarp();
     return r != 0;
 }
+// the whole warp waits, with one outcome
+__device__ __forceinline__ bool px_wait_all(uint64_t* b, uint32_t parity, volatile int* abort, unsigned long long limit) {
+    return __all_sync(0xffffffffu, px_wait(b, parity, abort, limit)) != 0;
+}
+__device__ __forceinline__ bool px_elect() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
 __device__ __forceinline__ void px_bar(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 
 struct PxTile { int g, m, row0, nvalid; };
@@ -149,8 +159,8 @@ __device__ __forceinline__ void px_load_scales(const uint8_t* row, int c, int ns
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             uint32_t lo = 0x7F7Fu, hi = 0x7F7Fu;
-            if (o + 4 * i < nsc) lo = row[o + 4 * i] | uint32_t(row[o + 4 * i + 1]) << 8;
-            if (o + 4 * i + 2 < nsc) hi = row[o + 4 * i + 2] | uint32_t(row[o + 4 * i + 3]) << 8;
+            if (o + 4 * i < nsc) lo = *reinterpret_cast<const uint16_t*>(row + o + 4 * i);
+            if (o + 4 * i + 2 < nsc) hi = *reinterpret_cast<const uint16_t*>(row + o + 4 * i + 2);
             v[i] = lo | hi << 16;
         }
     }
@@ -159,7 +169,8 @@ __device__ __forceinline__ void px_load_scales(const uint8_t* row, int c, int ns
 template <bool SWIGLU, int BN>
 __global__ void __launch_bounds__(kPxThreads, 1)
 mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_sw,
-                   const __grid_constant__ CUtensorMap tm_a, PxParams p) {
+                   const __grid_constant__ CUtensorMap tm_a1, const __grid_constant__ CUtensorMap tm_a2,
+                   const __grid_constant__ CUtensorMap tm_a4, PxParams p) {
     using C = PxCfg<BN>;
     constexpr int kSt = C::kStages;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -169,8 +180,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
     uint8_t* sSf = sB + kSt * C::kBBytes;
     uint8_t* sEpi = sSf + kSt * C::kSfBytes;
     uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + C::kEpiBytes);
-    uint64_t* sfull = full + kSt;
-    uint64_t* empty = sfull + kSt;
+    uint64_t* empty = full + kSt;
     uint64_t* tfull = empty + kSt;
     uint64_t* tempty = tfull + 2;
     uint64_t* mma_done = tempty + 2;
@@ -203,8 +213,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
     if (lane == 31) wsum[warp] = inc;
     if (tid == 0) {
         for (int s = 0; s < kSt; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&sfull[s], kPxLoaders);
+            mbar_init(&full[s], 1 + kPxLoaders);     // the stage's TMA bytes and its scale atoms
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -234,54 +243,74 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
     const int nk = p.nk;
 
     if (warp == 0) {
-        // ------------------------------------------------ TMA producer
-        if (lane == 0) {
-            int s = 0, step = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-                const PxTile tl = px_tile<BN>(t, ntile, off, G, p.m_tiles);
-                const bool shared_grp = tl.g >= p.E;
-                const CUtensorMap* mw = shared_grp ? &tm_sw : &tm_w;
-                const int wg = shared_grp ? 0 : tl.g;
-                const int nbox = (tl.nvalid + 31) >> 5;
-                const uint32_t bytes = uint32_t(kPxABytes) + uint32_t(nbox) * 4096u;
-                for (int kb = 0; kb < nk; ++kb, ++step) {
-                    if (!px_wait(&empty[s], phase ^ 1u, abort_flag, p.wait_ns)) { ok = false; break; }
+        // ------------------------------------------------ TMA producer (warp-uniform, one elected lane issues)
+        const int utotal = __shfl_sync(0xffffffffu, total, 0);
+        const bool leader = px_elect();
+        int s = 0, step = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < utotal && ok; t += gridDim.x) {
+            const PxTile tl = px_tile<BN>(t, ntile, off, G, p.m_tiles);
+            const int g = __shfl_sync(0xffffffffu, tl.g, 0), m = __shfl_sync(0xffffffffu, tl.m, 0);
+            const int row0 = __shfl_sync(0xffffffffu, tl.row0, 0);
+            const bool shared_grp = g >= p.E;
+            const CUtensorMap* mw = shared_grp ? &tm_sw : &tm_w;
+            const int wg = shared_grp ? 0 : g;
+            // the tile's rows in units of the smallest box, loaded as at most one box of each size
+            const int units = __shfl_sync(0xffffffffu, (tl.nvalid + C::kBox - 1) / C::kBox, 0);
+            const uint32_t bytes = uint32_t(kPxABytes) + uint32_t(units) * (C::kBox * 128u);
+            for (int kb = 0; kb < nk; ++kb, ++step) {
+                ok = px_wait_all(&empty[s], phase ^ 1u, abort_flag, p.wait_ns);
+                if (!ok) break;
+                if (leader) {
                     mbar_expect_tx(&full[s], bytes);
                     uint8_t* a = sA + s * kPxABytes;
-                    if (SWIGLU) tma_5d(mw, &full[s], a, kb * 128, 0, 0, tl.m * 4, wg);
-                    else tma_3d(mw, &full[s], a, kb * 128, tl.m * 128, wg);
-                    for (int b = 0; b < nbox; ++b)
-                        tma_2d(&tm_a, &full[s], sB + s * C::kBBytes + b * 4096, kb * 128, tl.row0 + 32 * b);
-                    if (++s == kSt) { s = 0; phase ^= 1u; }
+                    if (SWIGLU) tma_5d(mw, &full[s], a, kb * 128, 0, 0, m * 4, wg);
+                    else tma_3d(mw, &full[s], a, kb * 128, m * 128, wg);
+                    uint8_t* b = sB + s * C::kBBytes;
+                    int r = row0;
+                    if (BN > 32 && (units & 4)) { tma_2d(&tm_a4, &full[s], b, kb * 128, r); b += 4 * C::kBox * 128; r += 4 * C::kBox; }
+                    if (units & 2) { tma_2d(&tm_a2, &full[s], b, kb * 128, r); b += 2 * C::kBox * 128; r += 2 * C::kBox; }
+                    if (units & 1) tma_2d(&tm_a1, &full[s], b, kb * 128, r);
                 }
+                __syncwarp();
+                if (++s == kSt) { s = 0; phase ^= 1u; }
             }
+        }
+        if (leader) {
             if (!ok) { *abort_flag = 1; atomicExch(p.err, kDevErrTimeout); }
             for (int st = step > kSt ? step - kSt : 0; st < step; ++st)     // own copies in flight have landed
                 mbar_wait(&full[st % kSt], uint32_t(st / kSt) & 1u, nullptr);
         }
+        __syncwarp();
     } else if (warp == 1) {
-        // ------------------------------------------------ scale copies and MMAs, one thread
-        if (lane == 0) {
-            const uint64_t ad0 = sdesc_sw128(su32(sA)), bd0 = sdesc_sw128(su32(sB));
-            const uint64_t sf0 = px_atom_desc(su32(sSf));
-            int s = 0, j = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++j) {
-                const PxTile tl = px_tile<BN>(t, ntile, off, G, p.m_tiles);
-                const int N = (tl.nvalid + 15) & ~15;
-                const int buf = j & 1;
-                if (!px_wait(&tempty[buf], (uint32_t(j >> 1) & 1u) ^ 1u, abort_flag, p.wait_ns)) { ok = false; break; }
+        // ------------------------------------------------ scale copies and MMAs
+        // The whole warp runs the loop and one elected lane issues: with warp-uniform control flow the
+        // descriptors stay in uniform registers, where the tcgen05 instructions want them.  (Under
+        // `if (lane == 0)` every operand is moved there one by one: 1200 clocks a stage against
+        // PX_ISSUE_NOW.)
+        const int utotal = __shfl_sync(0xffffffffu, total, 0);
+        const bool leader = px_elect();
+        const uint64_t ad0 = sdesc_sw128(su32(sA)), bd0 = sdesc_sw128(su32(sB));
+        const uint64_t sf0 = px_atom_desc(su32(sSf));
+        int s = 0, j = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < utotal; t += gridDim.x, ++j) {
+            const PxTile tl = px_tile<BN>(t, ntile, off, G, p.m_tiles);
+            const int N = __shfl_sync(0xffffffffu, (tl.nvalid + 15) & ~15, 0);
+            const int buf = j & 1;
+            ok = px_wait_all(&tempty[buf], (uint32_t(j >> 1) & 1u) ^ 1u, abort_flag, p.wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t dacc = tmem + uint32_t(BN * buf);
+            const uint32_t id0 = idesc_mxf4(N, 0), id2 = idesc_mxf4(N, 2);
+            const bool two = C::kHalves == 2 && N > 128;
+            for (int kb = 0; kb < nk; ++kb) {
+                ok = px_wait_all(&full[s], phase, abort_flag, p.wait_ns);
+                if (!ok) break;
                 tc_fence_after();
-                const uint32_t dacc = tmem + uint32_t(BN * buf);
-                const uint32_t id0 = idesc_mxf4(N, 0), id2 = idesc_mxf4(N, 2);
-                const bool two = C::kHalves == 2 && N > 128;
-                for (int kb = 0; kb < nk; ++kb) {
-                    if (!px_wait(&full[s], phase, abort_flag, p.wait_ns) ||
-                        !px_wait(&sfull[s], phase, abort_flag, p.wait_ns)) { ok = false; break; }
-                    tc_fence_after();
+                if (leader) {
                     const uint32_t sfa = tmem + uint32_t(C::kSfBase + (s & 1) * C::kSfCols), sfb = sfa + 8u;
                     const uint64_t sd = sf0 + uint64_t((s * C::kSfBytes) >> 4);
 #pragma unroll
@@ -300,15 +329,20 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                                   (sfa + 4u * (i >> 1)) | hi, (sfb + 4u * C::kHalves * (i >> 1)) | hi, (kb | i) != 0);
                     }
                     umma_commit(&empty[s]);
-                    if (++s == kSt) { s = 0; phase ^= 1u; }
                 }
-                if (!ok) break;
-                umma_commit(&tfull[buf]);
+                __syncwarp();
+                if (++s == kSt) { s = 0; phase ^= 1u; }
             }
+            if (!ok) break;
+            if (leader) umma_commit(&tfull[buf]);
+            __syncwarp();
+        }
+        if (leader) {
             if (!ok) { *abort_flag = 1; atomicExch(p.err, kDevErrTimeout); }
             umma_commit(mma_done);
             mbar_wait(mma_done, 0, nullptr);
         }
+        __syncwarp();
     } else if (warp < 2 + kPxLoaders) {
         // ------------------------------------------------ scale bytes -> atoms, four stages per load
         // Thread i takes A row i and B rows i, i + 128; the next 32 bytes of each are in flight while
@@ -358,7 +392,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sfull[s]);
+                if (lane == 0) mbar_arrive(&full[s]);
                 if (++s == kSt) { s = 0; phase ^= 1u; }
             }
             t = tn;
@@ -481,27 +515,29 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
 }
 
 template <bool SWIGLU, int BN>
-static int launch_variant(int grid, cudaStream_t st, const CUtensorMap& tw, const CUtensorMap& tsw, const CUtensorMap& ta,
-                          const PxParams& p) {
+static int launch_variant(int grid, cudaStream_t st, const CUtensorMap& tw, const CUtensorMap& tsw,
+                          const CUtensorMap (&ta)[3], const PxParams& p) {
     constexpr size_t smem = PxCfg<BN>::smem();
     static PerDeviceOnce attr;
     if (attr([&] {
             return cudaFuncSetAttribute(mx4_product_kernel<SWIGLU, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
         }) != cudaSuccess)
         return 2;
-    mx4_product_kernel<SWIGLU, BN><<<grid, kPxThreads, smem, st>>>(tw, tsw, ta, p);
+    mx4_product_kernel<SWIGLU, BN><<<grid, kPxThreads, smem, st>>>(tw, tsw, ta[0], ta[1], ta[2], p);
     return cudaGetLastError() == cudaSuccess ? 0 : 2;
 }
 
 int launch_mx4_product(const Mx4Launch& L, cudaStream_t st) {
     const int wrows = L.swiglu ? 2 * L.N : L.N;        // weight rows per group
     const uint64_t kb = uint64_t(L.K) / 2;             // code bytes per row
-    CUtensorMap tw{}, tsw{}, ta{};
-    {
+    const bool small = L.R <= 16 * L.G;
+    CUtensorMap tw{}, tsw{}, ta[3]{};
+    for (int i = 0; i < 3; ++i) {
+        if (small && i == 2) { ta[2] = ta[1]; break; }     // BN = 32 has two sizes
         uint64_t dims[2] = {kb, uint64_t(L.R)};
         uint64_t str[1] = {kb};
-        uint32_t box[2] = {128, 32};
-        if (!make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, L.a, 2, dims, str, box)) return 1;
+        uint32_t box[2] = {128, uint32_t(small ? PxCfg<32>::kBox : PxCfg<224>::kBox) << i};
+        if (!make_map(&ta[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, L.a, 2, dims, str, box)) return 1;
     }
     auto weight_map = [&](CUtensorMap* m, const uint8_t* w, int groups) {
         if (L.swiglu) {
@@ -537,7 +573,6 @@ int launch_mx4_product(const Mx4Launch& L, cudaStream_t st) {
     const uintptr_t al = reinterpret_cast<uintptr_t>(L.ws) | reinterpret_cast<uintptr_t>(L.as) |
                          (L.G > L.E ? reinterpret_cast<uintptr_t>(L.sws) : 0) | uintptr_t(L.K / 32);
     p.vec = al % 16 == 0 ? 16 : al % 8 == 0 ? 8 : 2;
-    const bool small = L.R <= 16 * L.G;
     const int64_t bn = small ? 32 : 224;
     const int64_t tiles = int64_t(p.m_tiles) * (int64_t(L.G < L.R ? L.G : L.R) + L.R / bn);   // an upper bound
     const int grid = int(tiles < num_sms() ? tiles : num_sms());
