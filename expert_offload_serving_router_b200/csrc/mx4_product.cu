@@ -32,6 +32,7 @@ constexpr int kPxThreads = 448;
 constexpr int kPxLoaders = 4;                // scale warps
 constexpr int kPxEpi = 8;                    // epilogue warps
 constexpr int kPxK = 256;                    // K per stage: 128 bytes of codes per row
+constexpr int kPxChunk = 4;                  // stages per scale chunk: 32 scale bytes of a row
 constexpr int kPxABytes = 128 * 128;
 constexpr int kPxGroups = kMaxExperts + 1;
 constexpr int kPxHRow = 65;                  // fp32 per token row of the h buffer: 64 + 1 against bank conflicts
@@ -43,13 +44,14 @@ struct PxCfg {
     static constexpr int kBBytes = BN * 128;
     static constexpr int kBox = BN == 32 ? 16 : 32;                // rows of the smallest activation box; the others are 2x, 4x
     static constexpr int kSfA = 2 * 512;
-    static constexpr int kSfBytes = kSfA + 2 * kHalves * 512;
+    static constexpr int kSfBytes = kSfA + 2 * kHalves * 512;      // scale atoms of one stage
+    static constexpr int kSfChunk = kPxChunk * kSfBytes;           // of one chunk; two chunk buffers
     static constexpr int kSfCols = 2 * 4 + 2 * 4 * kHalves;        // TMEM columns of one stage's scales
     static constexpr int kSfBase = 2 * BN;                         // after the two accumulators
     static constexpr int kTmemCols = BN == 32 ? 128 : 512;
     static constexpr int kEpiBytes = 2 * 32 * kPxHRow * 4;         // >= 8 x 2 KB transpose buffers
     static constexpr size_t smem() {
-        return 1024 + size_t(kStages) * (kPxABytes + kBBytes + kSfBytes) + kEpiBytes + (2 * kStages + 8) * 8 +
+        return 1024 + size_t(kStages) * (kPxABytes + kBBytes) + 2 * kSfChunk + kEpiBytes + (2 * kStages + 12) * 8 +
                (2 * (kPxGroups + 1) + 32) * 4;
     }
     static_assert(kSfBase + 2 * kSfCols <= kTmemCols, "TMEM columns");
@@ -59,7 +61,7 @@ struct PxCfg {
 struct PxParams {
     int K, nk, m_tiles, G, E, R;
     int N;                    // bf16 output columns, or weight rows per group with SwiGLU (2F)
-    int vec;                  // bytes a scale load may take: 16, 8 or 2
+    int vec;                  // 16: scale rows start on 16-byte boundaries; else 2
     const int32_t* offsets;
     const uint8_t* wsc;
     const uint8_t* swsc;
@@ -135,33 +137,31 @@ __device__ __forceinline__ PxTile px_tile(int t, const int* ntile, const int* of
     return r;
 }
 
-// 32 scale bytes (1024 elements) of a row from byte 32 c on; bytes past the row's nsc are 127 (2^0)
-__device__ __forceinline__ void px_load_scales(const uint8_t* row, int c, int nsc, int vec, bool valid, uint32_t (&v)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0x7F7F7F7Fu;
-    if (!valid) return;
-    const int o = 32 * c;
+// 32 scale bytes (1024 elements) of a row, from byte 32 c on.  Bytes past the row's nsc are whatever
+// is there: the MMAs stop at K.  Rows that start off an 8-byte boundary (K / 32 not a multiple of 8)
+// are read as the aligned 8-byte words that hold them and shifted into place -- a word is read
+// only if it holds a byte of the row, so no read leaves the allocation.
+__device__ __forceinline__ void px_load_scales(const uint8_t* row, int c, int nsc, int vec, uint32_t (&v)[8]) {
+    const int o = 32 * c, n = min(32, nsc - o);
     if (vec == 16) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            if (o + 16 * i < nsc) {
+            if (16 * i < n) {
                 const uint4 u = *reinterpret_cast<const uint4*>(row + o + 16 * i);
                 v[4 * i] = u.x; v[4 * i + 1] = u.y; v[4 * i + 2] = u.z; v[4 * i + 3] = u.w;
             }
-    } else if (vec == 8) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (o + 8 * i < nsc) {
-                const uint2 u = *reinterpret_cast<const uint2*>(row + o + 8 * i);
-                v[2 * i] = u.x; v[2 * i + 1] = u.y;
-            }
     } else {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(row + o);
+        const uint64_t* w = reinterpret_cast<const uint64_t*>(at & ~uintptr_t(7));
+        const int lead = int(at & 7), sh = 8 * lead;
+        uint64_t u[5];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            uint32_t lo = 0x7F7Fu, hi = 0x7F7Fu;
-            if (o + 4 * i < nsc) lo = *reinterpret_cast<const uint16_t*>(row + o + 4 * i);
-            if (o + 4 * i + 2 < nsc) hi = *reinterpret_cast<const uint16_t*>(row + o + 4 * i + 2);
-            v[i] = lo | hi << 16;
+        for (int i = 0; i < 5; ++i) u[i] = 8 * i < lead + n ? w[i] : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint64_t x = sh ? (u[i] >> sh) | (u[i + 1] << (64 - sh)) : u[i];
+            v[2 * i] = uint32_t(x);
+            v[2 * i + 1] = uint32_t(x >> 32);
         }
     }
 }
@@ -178,12 +178,14 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
     uint8_t* sA = smem;
     uint8_t* sB = sA + kSt * kPxABytes;
     uint8_t* sSf = sB + kSt * C::kBBytes;
-    uint8_t* sEpi = sSf + kSt * C::kSfBytes;
+    uint8_t* sEpi = sSf + 2 * C::kSfChunk;
     uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + C::kEpiBytes);
     uint64_t* empty = full + kSt;
     uint64_t* tfull = empty + kSt;
     uint64_t* tempty = tfull + 2;
-    uint64_t* mma_done = tempty + 2;
+    uint64_t* sfull = tempty + 2;
+    uint64_t* sempty = sfull + 2;
+    uint64_t* mma_done = sempty + 2;
     int* ntile = reinterpret_cast<int*>(mma_done + 1);      // [G + 1] first row tile of each group
     int* off = ntile + kPxGroups + 1;                       // [G + 1] row offsets
     int* wsum = off + kPxGroups + 1;                        // block scan, then the epilogue's wait outcomes
@@ -213,12 +215,14 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
     if (lane == 31) wsum[warp] = inc;
     if (tid == 0) {
         for (int s = 0; s < kSt; ++s) {
-            mbar_init(&full[s], 1 + kPxLoaders);     // the stage's TMA bytes and its scale atoms
+            mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
             mbar_init(&tempty[b], kPxEpi);
+            mbar_init(&sfull[b], kPxLoaders);
+            mbar_init(&sempty[b], 1);
         }
         mbar_init(mma_done, 1);
         *abort_flag = 0;
@@ -293,7 +297,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
         const bool leader = px_elect();
         const uint64_t ad0 = sdesc_sw128(su32(sA)), bd0 = sdesc_sw128(su32(sB));
         const uint64_t sf0 = px_atom_desc(su32(sSf));
-        int s = 0, j = 0;
+        int s = 0, j = 0, ch = 0;             // stage, tile and scale chunk counters
         uint32_t phase = 0;
         bool ok = true;
         for (int t = blockIdx.x; t < utotal; t += gridDim.x, ++j) {
@@ -307,12 +311,17 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
             const uint32_t id0 = idesc_mxf4(N, 0), id2 = idesc_mxf4(N, 2);
             const bool two = C::kHalves == 2 && N > 128;
             for (int kb = 0; kb < nk; ++kb) {
+                if ((kb & (kPxChunk - 1)) == 0) {
+                    ok = px_wait_all(&sfull[ch & 1], uint32_t(ch >> 1) & 1u, abort_flag, p.wait_ns);
+                    if (!ok) break;
+                }
                 ok = px_wait_all(&full[s], phase, abort_flag, p.wait_ns);
                 if (!ok) break;
                 tc_fence_after();
+                const bool chunk_end = (kb & (kPxChunk - 1)) == kPxChunk - 1 || kb == nk - 1;
                 if (leader) {
                     const uint32_t sfa = tmem + uint32_t(C::kSfBase + (s & 1) * C::kSfCols), sfb = sfa + 8u;
-                    const uint64_t sd = sf0 + uint64_t((s * C::kSfBytes) >> 4);
+                    const uint64_t sd = sf0 + uint64_t(((ch & 1) * C::kSfChunk + (kb & (kPxChunk - 1)) * C::kSfBytes) >> 4);
 #pragma unroll
                     for (int a = 0; a < 2; ++a) {
                         px_copy_atom(sfa + 4u * a, sd + uint64_t(32 * a));
@@ -329,8 +338,10 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                                   (sfa + 4u * (i >> 1)) | hi, (sfb + 4u * C::kHalves * (i >> 1)) | hi, (kb | i) != 0);
                     }
                     umma_commit(&empty[s]);
+                    if (chunk_end) umma_commit(&sempty[ch & 1]);
                 }
                 __syncwarp();
+                if (chunk_end) ++ch;
                 if (++s == kSt) { s = 0; phase ^= 1u; }
             }
             if (!ok) break;
@@ -344,11 +355,12 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
         }
         __syncwarp();
     } else if (warp < 2 + kPxLoaders) {
-        // ------------------------------------------------ scale bytes -> atoms, four stages per load
-        // Thread i takes A row i and B rows i, i + 128; the next 32 bytes of each are in flight while
-        // the current ones are laid out.
+        // ------------------------------------------------ scale bytes -> atoms, a chunk (four stages) at a time
+        // Thread i takes A row i and B rows i, i + 128: 32 bytes of each, the next chunk's in flight
+        // while the current one waits for its buffer and is laid out.  One proxy fence and one arrival
+        // per chunk: per stage they made this warp the pipeline's slowest.
         const int i = tid - 64;
-        const int nsc = p.K / 32, nch = (nk + 3) >> 2;
+        const int nsc = p.K / 32, nch = (nk + kPxChunk - 1) / kPxChunk;
         const int at = 16 * (i & 31) + 4 * (i >> 5);
         uint32_t cur[1 + C::kHalves][8], nxt[1 + C::kHalves][8];
         auto load = [&](int t, int c, uint32_t (&v)[1 + C::kHalves][8]) {
@@ -359,42 +371,36 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                 const int F = p.N >> 1, f = tl.m * 64 + 16 * (i >> 5) + (i & 15);
                 wrow = (i & 31) < 16 ? f : F + f;
             } else {
-                wrow = tl.m * 128 + i;
+                wrow = min(tl.m * 128 + i, p.N - 1);
             }
-            const uint8_t* wr = (shared_grp ? p.swsc : p.wsc) + (size_t(shared_grp ? 0 : tl.g) * p.N + wrow) * nsc;
-            px_load_scales(wr, c, nsc, p.vec, wrow < p.N, v[0]);
+            px_load_scales((shared_grp ? p.swsc : p.wsc) + (size_t(shared_grp ? 0 : tl.g) * p.N + wrow) * nsc, c, nsc, p.vec, v[0]);
 #pragma unroll
-            for (int h = 0; h < C::kHalves; ++h) {
-                const int r = i + 128 * h;
-                px_load_scales(p.asc + size_t(tl.row0 + r) * nsc, c, nsc, p.vec, r < tl.nvalid, v[1 + h]);
-            }
+            for (int h = 0; h < C::kHalves; ++h)
+                if (i + 128 * h < ((tl.nvalid + 15) & ~15))
+                    px_load_scales(p.asc + size_t(tl.row0 + min(i + 128 * h, tl.nvalid - 1)) * nsc, c, nsc, p.vec, v[1 + h]);
         };
-        int s = 0;
-        uint32_t phase = 0;
         bool ok = true;
-        int t = blockIdx.x, c = 0;
+        int t = blockIdx.x, c = 0, ch = 0;
         if (t < total) load(t, 0, cur);
-        while (t < total && ok) {
+        while (t < total) {
             int tn = t, cn = c + 1;
             if (cn == nch) { cn = 0; tn += gridDim.x; }
             if (tn < total) load(tn, cn, nxt);
+            if (!px_warp_wait(&sempty[ch & 1], (uint32_t(ch >> 1) & 1u) ^ 1u, abort_flag, p.wait_ns)) { ok = false; break; }
+            uint8_t* d = sSf + (ch & 1) * C::kSfChunk + at;
 #pragma unroll
-            for (int sub = 0; sub < 4; ++sub) {
-                if (4 * c + sub >= nk || !ok) break;
-                if (!px_warp_wait(&empty[s], phase ^ 1u, abort_flag, p.wait_ns)) { ok = false; break; }
-                uint8_t* d = sSf + s * C::kSfBytes + at;
+            for (int sub = 0; sub < kPxChunk; ++sub)
 #pragma unroll
                 for (int a = 0; a < 2; ++a) {
-                    *reinterpret_cast<uint32_t*>(d + 512 * a) = cur[0][2 * sub + a];
+                    *reinterpret_cast<uint32_t*>(d + sub * C::kSfBytes + 512 * a) = cur[0][2 * sub + a];
 #pragma unroll
                     for (int h = 0; h < C::kHalves; ++h)
-                        *reinterpret_cast<uint32_t*>(d + C::kSfA + (a * C::kHalves + h) * 512) = cur[1 + h][2 * sub + a];
+                        *reinterpret_cast<uint32_t*>(d + sub * C::kSfBytes + C::kSfA + (a * C::kHalves + h) * 512) = cur[1 + h][2 * sub + a];
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[s]);
-                if (++s == kSt) { s = 0; phase ^= 1u; }
-            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sfull[ch & 1]);
+            ++ch;
             t = tn;
             c = cn;
 #pragma unroll
@@ -572,7 +578,7 @@ int launch_mx4_product(const Mx4Launch& L, cudaStream_t st) {
     p.wait_ns = gemm_wait_ns();
     const uintptr_t al = reinterpret_cast<uintptr_t>(L.ws) | reinterpret_cast<uintptr_t>(L.as) |
                          (L.G > L.E ? reinterpret_cast<uintptr_t>(L.sws) : 0) | uintptr_t(L.K / 32);
-    p.vec = al % 16 == 0 ? 16 : al % 8 == 0 ? 8 : 2;
+    p.vec = al % 16 == 0 ? 16 : 2;
     const int64_t bn = small ? 32 : 224;
     const int64_t tiles = int64_t(p.m_tiles) * (int64_t(L.G < L.R ? L.G : L.R) + L.R / bn);   // an upper bound
     const int grid = int(tiles < num_sms() ? tiles : num_sms());
