@@ -28,8 +28,8 @@
 
 namespace ftmoe {
 
-constexpr int kPxThreads = 448;
-constexpr int kPxLoaders = 4;                // scale warps
+constexpr int kPxThreads = 576;
+constexpr int kPxLoaders = 8;                // scale warps: two groups of four, one per chunk buffer
 constexpr int kPxEpi = 8;                    // epilogue warps
 constexpr int kPxK = 256;                    // K per stage: 128 bytes of codes per row
 constexpr int kPxChunk = 4;                  // stages per scale chunk: 32 scale bytes of a row
@@ -221,7 +221,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
             mbar_init(&tempty[b], kPxEpi);
-            mbar_init(&sfull[b], kPxLoaders);
+            mbar_init(&sfull[b], kPxLoaders / 2);
             mbar_init(&sempty[b], 1);
         }
         mbar_init(mma_done, 1);
@@ -291,8 +291,8 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
         // ------------------------------------------------ scale copies and MMAs
         // The whole warp runs the loop and one elected lane issues: with warp-uniform control flow the
         // descriptors stay in uniform registers, where the tcgen05 instructions want them.  (Under
-        // `if (lane == 0)` every operand is moved there one by one: 1200 clocks a stage against
-        // PX_ISSUE_NOW.)
+        // `if (lane == 0)` every operand is moved there one by one: 1200 clocks a stage of N = 192
+        // against under 800.)
         const int utotal = __shfl_sync(0xffffffffu, total, 0);
         const bool leader = px_elect();
         const uint64_t ad0 = sdesc_sw128(su32(sA)), bd0 = sdesc_sw128(su32(sB));
@@ -356,57 +356,68 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
         __syncwarp();
     } else if (warp < 2 + kPxLoaders) {
         // ------------------------------------------------ scale bytes -> atoms, a chunk (four stages) at a time
-        // Thread i takes A row i and B rows i, i + 128: 32 bytes of each, the next chunk's in flight
-        // while the current one waits for its buffer and is laid out.  One proxy fence and one arrival
-        // per chunk: per stage they made this warp the pipeline's slowest.
-        const int i = tid - 64;
+        // Two groups of four warps take alternate chunks, a buffer each; thread i of a group takes A row i
+        // and B rows i, i + 128, 32 bytes of each.  A chunk's loads are issued right after the group's
+        // last one was laid out, so they have two chunks' MMA time to arrive.  (One group took a
+        // memory latency per chunk, and deeper register queues did not help: their loads share scoreboards.
+        // 129 groups of 143 rows, N 1408, K 2816: 82 -> 72 us.)
+        // One proxy fence and one arrival per chunk: per stage they made this warp the slowest.
+        const int grp = (warp - 2) >> 2, i = (tid - 64) & 127;
         const int nsc = p.K / 32, nch = (nk + kPxChunk - 1) / kPxChunk;
         const int at = 16 * (i & 31) + 4 * (i >> 5);
-        uint32_t cur[1 + C::kHalves][8], nxt[1 + C::kHalves][8];
-        auto load = [&](int t, int c, uint32_t (&v)[1 + C::kHalves][8]) {
-            const PxTile tl = px_tile<BN>(t, ntile, off, G, p.m_tiles);
-            const bool shared_grp = tl.g >= p.E;
-            int wrow;
-            if (SWIGLU) {
-                const int F = p.N >> 1, f = tl.m * 64 + 16 * (i >> 5) + (i & 15);
-                wrow = (i & 31) < 16 ? f : F + f;
-            } else {
-                wrow = min(tl.m * 128 + i, p.N - 1);
-            }
-            px_load_scales((shared_grp ? p.swsc : p.wsc) + (size_t(shared_grp ? 0 : tl.g) * p.N + wrow) * nsc, c, nsc, p.vec, v[0]);
+        constexpr int kRows = 1 + C::kHalves;
+        uint32_t v[kRows][8] = {};
+        int lt = blockIdx.x, lc = 0, cur = -1;      // the load cursor, and the tile its row pointers are of
+        const uint8_t* src[kRows] = {};
+        bool take[kRows] = {};
+        auto advance = [&](int n) {
+            for (lc += n; lc >= nch; lc -= nch) lt += gridDim.x;
+        };
+        auto load = [&]() {
+            if (lt >= total) return;
+            if (lt != cur) {
+                cur = lt;
+                const PxTile tl = px_tile<BN>(lt, ntile, off, G, p.m_tiles);
+                const bool shared_grp = tl.g >= p.E;
+                int wrow;
+                if (SWIGLU) {
+                    const int F = p.N >> 1, f = tl.m * 64 + 16 * (i >> 5) + (i & 15);
+                    wrow = (i & 31) < 16 ? f : F + f;
+                } else {
+                    wrow = min(tl.m * 128 + i, p.N - 1);
+                }
+                src[0] = (shared_grp ? p.swsc : p.wsc) + (size_t(shared_grp ? 0 : tl.g) * p.N + wrow) * nsc;
+                take[0] = true;
 #pragma unroll
-            for (int h = 0; h < C::kHalves; ++h)
-                if (i + 128 * h < ((tl.nvalid + 15) & ~15))
-                    px_load_scales(p.asc + size_t(tl.row0 + min(i + 128 * h, tl.nvalid - 1)) * nsc, c, nsc, p.vec, v[1 + h]);
+                for (int h = 0; h < C::kHalves; ++h) {
+                    take[1 + h] = i + 128 * h < ((tl.nvalid + 15) & ~15);
+                    src[1 + h] = p.asc + size_t(tl.row0 + min(i + 128 * h, tl.nvalid - 1)) * nsc;
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+                if (take[r]) px_load_scales(src[r], lc, nsc, p.vec, v[r]);
         };
         bool ok = true;
-        int t = blockIdx.x, c = 0, ch = 0;
-        if (t < total) load(t, 0, cur);
-        while (t < total) {
-            int tn = t, cn = c + 1;
-            if (cn == nch) { cn = 0; tn += gridDim.x; }
-            if (tn < total) load(tn, cn, nxt);
-            if (!px_warp_wait(&sempty[ch & 1], (uint32_t(ch >> 1) & 1u) ^ 1u, abort_flag, p.wait_ns)) { ok = false; break; }
-            uint8_t* d = sSf + (ch & 1) * C::kSfChunk + at;
+        advance(grp);
+        load();
+        for (uint32_t n = 0; lt < total; ++n) {
+            if (!px_warp_wait(&sempty[grp], (n & 1u) ^ 1u, abort_flag, p.wait_ns)) { ok = false; break; }
+            uint8_t* d = sSf + grp * C::kSfChunk + at;
 #pragma unroll
             for (int sub = 0; sub < kPxChunk; ++sub)
 #pragma unroll
                 for (int a = 0; a < 2; ++a) {
-                    *reinterpret_cast<uint32_t*>(d + sub * C::kSfBytes + 512 * a) = cur[0][2 * sub + a];
+                    *reinterpret_cast<uint32_t*>(d + sub * C::kSfBytes + 512 * a) = v[0][2 * sub + a];
 #pragma unroll
                     for (int h = 0; h < C::kHalves; ++h)
-                        *reinterpret_cast<uint32_t*>(d + sub * C::kSfBytes + C::kSfA + (a * C::kHalves + h) * 512) = cur[1 + h][2 * sub + a];
+                        *reinterpret_cast<uint32_t*>(d + sub * C::kSfBytes + C::kSfA + (a * C::kHalves + h) * 512) = v[1 + h][2 * sub + a];
                 }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sfull[ch & 1]);
-            ++ch;
-            t = tn;
-            c = cn;
-#pragma unroll
-            for (int h = 0; h < 1 + C::kHalves; ++h)
-#pragma unroll
-                for (int x = 0; x < 8; ++x) cur[h][x] = nxt[h][x];
+            if (lane == 0) mbar_arrive(&sfull[grp]);
+            advance(2);
+            load();
         }
         if (!ok) { *abort_flag = 1; if (lane == 0) atomicExch(p.err, kDevErrTimeout); }
     } else {
