@@ -23,6 +23,7 @@
 // 4 (row / 32) + j = row's scale of the step's block j); warps 6-13 epilogue, two per TMEM lane quarter.
 // The MMA thread copies a stage's atoms into TMEM right before the stage's MMAs (copies and MMAs of one
 // thread complete in issue order).  Every wait is bounded.
+#include "decode_common.cuh"
 #include "gemm_common.cuh"
 #include "mx4.cuh"
 
@@ -263,19 +264,36 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
             // the tile's rows in units of the smallest box, loaded as at most one box of each size
             const int units = __shfl_sync(0xffffffffu, (tl.nvalid + C::kBox - 1) / C::kBox, 0);
             const uint32_t bytes = uint32_t(kPxABytes) + uint32_t(units) * (C::kBox * 128u);
+            const auto load_w = [&](int kb, int s) {
+                mbar_expect_tx(&full[s], bytes);
+                uint8_t* a = sA + s * kPxABytes;
+                if (SWIGLU) tma_5d(mw, &full[s], a, kb * 128, 0, 0, m * 4, wg);
+                else tma_3d(mw, &full[s], a, kb * 128, m * 128, wg);
+            };
+            const auto load_a = [&](int kb, int s) {
+                uint8_t* b = sB + s * C::kBBytes;
+                int r = row0;
+                if (BN > 32 && (units & 4)) { tma_2d(&tm_a4, &full[s], b, kb * 128, r); b += 4 * C::kBox * 128; r += 4 * C::kBox; }
+                if (units & 2) { tma_2d(&tm_a2, &full[s], b, kb * 128, r); b += 2 * C::kBox * 128; r += 2 * C::kBox; }
+                if (units & 1) tma_2d(&tm_a1, &full[s], b, kb * 128, r);
+            };
+            int early = 0;                     // stages whose weights are already on their way
+            if (step == 0) {
+                // the ring's first round: weights before the wait for the kernel that writes the activations
+                early = min(kSt, nk);
+                if (leader) {
+                    for (int kb = 0; kb < early; ++kb) load_w(kb, kb);
+                    pdl_wait();
+                    pdl_trigger();             // after the wait: what this kernel waited for is final for its dependent too
+                }
+                __syncwarp();
+            }
             for (int kb = 0; kb < nk; ++kb, ++step) {
                 ok = px_wait_all(&empty[s], phase ^ 1u, abort_flag, p.wait_ns);
                 if (!ok) break;
                 if (leader) {
-                    mbar_expect_tx(&full[s], bytes);
-                    uint8_t* a = sA + s * kPxABytes;
-                    if (SWIGLU) tma_5d(mw, &full[s], a, kb * 128, 0, 0, m * 4, wg);
-                    else tma_3d(mw, &full[s], a, kb * 128, m * 128, wg);
-                    uint8_t* b = sB + s * C::kBBytes;
-                    int r = row0;
-                    if (BN > 32 && (units & 4)) { tma_2d(&tm_a4, &full[s], b, kb * 128, r); b += 4 * C::kBox * 128; r += 4 * C::kBox; }
-                    if (units & 2) { tma_2d(&tm_a2, &full[s], b, kb * 128, r); b += 2 * C::kBox * 128; r += 2 * C::kBox; }
-                    if (units & 1) tma_2d(&tm_a1, &full[s], b, kb * 128, r);
+                    if (kb >= early) load_w(kb, s);
+                    load_a(kb, s);
                 }
                 __syncwarp();
                 if (++s == kSt) { s = 0; phase ^= 1u; }
@@ -399,6 +417,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                 if (take[r]) px_load_scales(src[r], lc, nsc, p.vec, v[r]);
         };
         bool ok = true;
+        pdl_wait();                            // the activations' scales come from the preceding kernel
         advance(grp);
         load();
         for (uint32_t n = 0; lt < total; ++n) {
@@ -532,7 +551,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
 }
 
 template <bool SWIGLU, int BN>
-static int launch_variant(int grid, cudaStream_t st, const CUtensorMap& tw, const CUtensorMap& tsw,
+static int launch_variant(int grid, bool dependent, cudaStream_t st, const CUtensorMap& tw, const CUtensorMap& tsw,
                           const CUtensorMap (&ta)[3], const PxParams& p) {
     constexpr size_t smem = PxCfg<BN>::smem();
     static PerDeviceOnce attr;
@@ -540,8 +559,17 @@ static int launch_variant(int grid, cudaStream_t st, const CUtensorMap& tw, cons
             return cudaFuncSetAttribute(mx4_product_kernel<SWIGLU, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
         }) != cudaSuccess)
         return 2;
-    mx4_product_kernel<SWIGLU, BN><<<grid, kPxThreads, smem, st>>>(tw, tsw, ta[0], ta[1], ta[2], p);
-    return cudaGetLastError() == cudaSuccess ? 0 : 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kPxThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = dependent ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, mx4_product_kernel<SWIGLU, BN>, tw, tsw, ta[0], ta[1], ta[2], p) == cudaSuccess ? 0 : 2;
 }
 
 int launch_mx4_product(const Mx4Launch& L, cudaStream_t st) {
@@ -593,8 +621,10 @@ int launch_mx4_product(const Mx4Launch& L, cudaStream_t st) {
     const int64_t bn = small ? 32 : 224;
     const int64_t tiles = int64_t(p.m_tiles) * (int64_t(L.G < L.R ? L.G : L.R) + L.R / bn);   // an upper bound
     const int grid = int(tiles < num_sms() ? tiles : num_sms());
-    if (L.swiglu) return small ? launch_variant<true, 32>(grid, st, tw, tsw, ta, p) : launch_variant<true, 224>(grid, st, tw, tsw, ta, p);
-    return small ? launch_variant<false, 32>(grid, st, tw, tsw, ta, p) : launch_variant<false, 224>(grid, st, tw, tsw, ta, p);
+    const bool dep = L.dependent != 0;
+    if (L.swiglu)
+        return small ? launch_variant<true, 32>(grid, dep, st, tw, tsw, ta, p) : launch_variant<true, 224>(grid, dep, st, tw, tsw, ta, p);
+    return small ? launch_variant<false, 32>(grid, dep, st, tw, tsw, ta, p) : launch_variant<false, 224>(grid, dep, st, tw, tsw, ta, p);
 }
 
 }  // namespace ftmoe

@@ -4,6 +4,7 @@
 // One pass, bound by memory: a thread takes eight consecutive elements (one or two 16-byte loads),
 // four neighbouring lanes share a 32-element block and exchange its maximum with two shuffles;
 // kIlp vectors per thread are loaded before the first is used.
+#include "decode_common.cuh"
 #include "mx4.cuh"
 
 namespace ftmoe {
@@ -167,6 +168,8 @@ __global__ void __launch_bounds__(kQThreads) mx4_sorted_tokens_kernel(int T, int
     const int64_t id = at < total ? at : 0;
     const int t = int(id <= 0xFFFFFFFFll ? int64_t(uint32_t(id) / uint32_t(nv)) : id / nv);
     const int c = int(id - int64_t(t) * nv);
+    pdl_wait();
+    pdl_trigger();      // after the wait: the permutation is final for the product that follows
     const uint4 u[1] = {ldg_nc_v4(reinterpret_cast<const uint4*>(x) + id)};
     int pos[kMaxTopK + 1];
 #pragma unroll
@@ -186,13 +189,20 @@ __global__ void __launch_bounds__(kQThreads) mx4_sorted_tokens_kernel(int T, int
 }
 
 cudaError_t launch_mx4_sorted_tokens(int T, int H, int k, int S, const uint16_t* x, const int32_t* inv_pos,
-                                     uint8_t* codes, uint8_t* scales, cudaStream_t st) {
+                                     uint8_t* codes, uint8_t* scales, bool dependent, cudaStream_t st) {
     if (T <= 0) return cudaSuccess;
     const int nv = H / 8;
     const int64_t blocks = (int64_t(T) * nv + kQThreads - 1) / kQThreads;
-    mx4_sorted_tokens_kernel<<<unsigned(blocks), kQThreads, 0, st>>>(T, nv, k, S, x, inv_pos,
-                                                                     reinterpret_cast<uint32_t*>(codes), scales);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(blocks));
+    cfg.blockDim = dim3(kQThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = dependent ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, mx4_sorted_tokens_kernel, T, nv, k, S, x, inv_pos, reinterpret_cast<uint32_t*>(codes), scales);
 }
 
 }  // namespace ftmoe
