@@ -94,7 +94,7 @@ static ft_status check_product(int32_t groups, int32_t rows, int32_t n, int32_t 
     if (groups > kMaxExperts) return fail(FT_ERR_UNSUPPORTED, "groups %d > %d", groups, kMaxExperts);
     if (k % 64 || k > 16384) return fail(FT_ERR_UNSUPPORTED, "k %d: need k %% 64 == 0, k <= 16384", k);
     if (n % 8) return fail(FT_ERR_UNSUPPORTED, "n %d: need n %% 8 == 0", n);
-    if ((int64_t(rows) / 32 + groups + 1) * ((n + 127) / 128) > 0x7FFFFFFFll || n > (1 << 24))
+    if ((int64_t(rows) / 32 + groups + 1) * ((n + 127) / 128) > 0x7FFFFFFFll || n > (1 << 22))
         return fail(FT_ERR_UNSUPPORTED, "rows %d x n %d is too large for one call", rows, n);
     return FT_OK;
 }

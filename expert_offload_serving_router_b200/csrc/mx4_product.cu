@@ -34,26 +34,28 @@ constexpr int kPxLoaders = 8;                // scale warps: two groups of four,
 constexpr int kPxEpi = 8;                    // epilogue warps
 constexpr int kPxK = 256;                    // K per stage: 128 bytes of codes per row
 constexpr int kPxChunk = 4;                  // stages per scale chunk: 32 scale bytes of a row
+constexpr int kPxSfBufs = 4;                 // chunk buffers
 constexpr int kPxABytes = 128 * 128;
 constexpr int kPxGroups = kMaxExperts + 1;
+constexpr int kPxTable = 256;                // tiles of a CTA (pair) worked out ahead
 constexpr int kPxHRow = 65;                  // fp32 per token row of the h buffer: 64 + 1 against bank conflicts
 
-template <int BN>
+template <int BN, bool PAIR>
 struct PxCfg {
-    static constexpr int kStages = BN == 32 ? 8 : 4;
+    static constexpr int kStages = BN == 32 ? 8 : PAIR ? 5 : 3;
     static constexpr int kHalves = BN > 128 ? 2 : 1;               // 128-row scale atoms of B per 128-deep K step
-    static constexpr int kBBytes = BN * 128;
-    static constexpr int kBox = BN == 32 ? 16 : 32;                // rows of the smallest activation box; the others are 2x, 4x
+    static constexpr int kBBytes = (PAIR ? BN / 2 : BN) * 128;     // a pair's CTA loads half of the rows
+    static constexpr int kBox = BN == 32 || PAIR ? 16 : 32;                // rows of the smallest activation box; the others are 2x, 4x
     static constexpr int kSfA = 2 * 512;
     static constexpr int kSfBytes = kSfA + 2 * kHalves * 512;      // scale atoms of one stage
-    static constexpr int kSfChunk = kPxChunk * kSfBytes;           // of one chunk; two chunk buffers
+    static constexpr int kSfChunk = kPxChunk * kSfBytes;           // of one chunk
     static constexpr int kSfCols = 2 * 4 + 2 * 4 * kHalves;        // TMEM columns of one stage's scales
     static constexpr int kSfBase = 2 * BN;                         // after the two accumulators
     static constexpr int kTmemCols = BN == 32 ? 128 : 512;
     static constexpr int kEpiBytes = 2 * 32 * kPxHRow * 4;         // >= 8 x 2 KB transpose buffers
     static constexpr size_t smem() {
-        return 1024 + size_t(kStages) * (kPxABytes + kBBytes) + 2 * kSfChunk + kEpiBytes + (2 * kStages + 12) * 8 +
-               (2 * (kPxGroups + 1) + 32) * 4;
+        return 1024 + size_t(kStages) * (kPxABytes + kBBytes) + kPxSfBufs * kSfChunk + kEpiBytes + (2 * kStages + 2 * kPxSfBufs + 8) * 8 +
+               (2 * (kPxGroups + 1) + 32) * 4 + kPxTable * 8;
     }
     static_assert(kSfBase + 2 * kSfCols <= kTmemCols, "TMEM columns");
     static_assert(kEpiBytes >= kPxEpi * kXposeBytes, "epilogue buffers");
@@ -74,26 +76,40 @@ struct PxParams {
     unsigned long long wait_ns;
 };
 
-// kind::mxf4 instruction descriptor: E2M1 x E2M1, both K-major, E8M0 scales, M = 128; the scale
-// ids (0 or 2) select which two of a column word's four scale bytes the 64-deep MMA takes
-__device__ __forceinline__ uint32_t idesc_mxf4(int N, uint32_t sf_id) {
-    return (sf_id << 4) | (1u << 7) | (1u << 10) | (uint32_t(N >> 3) << 17) | (1u << 23) | (uint32_t(128 >> 4) << 24) |
+// kind::mxf4 instruction descriptor: E2M1 x E2M1, both K-major, E8M0 scales, M = 128 (256 for a
+// pair); the scale ids (0 or 2) select which two of a column word's four scale bytes the 64-deep MMA takes
+__device__ __forceinline__ uint32_t idesc_mxf4(int M, int N, uint32_t sf_id) {
+    return (sf_id << 4) | (1u << 7) | (1u << 10) | (uint32_t(N >> 3) << 17) | (1u << 23) | (uint32_t(M >> 4) << 24) |
            (sf_id << 29);
 }
+template <bool PAIR>
 __device__ __forceinline__ void umma_mxf4(uint32_t dtm, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t tsfa,
                                           uint32_t tsfb, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
-        ::"r"(dtm), "l"(ad), "l"(bd), "r"(idesc), "r"(acc), "r"(tsfa), "r"(tsfb));
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+            ::"r"(dtm), "l"(ad), "l"(bd), "r"(idesc), "r"(acc), "r"(tsfa), "r"(tsfb));
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+            ::"r"(dtm), "l"(ad), "l"(bd), "r"(idesc), "r"(acc), "r"(tsfa), "r"(tsfb));
 }
 // source descriptor of a scale atom (contiguous, no swizzle) and its copy to four TMEM columns,
 // repeated in every lane quarter
 __device__ __forceinline__ uint64_t px_atom_desc(uint32_t saddr) {
     return uint64_t((saddr >> 4) & 0x3FFFu) | uint64_t(128 >> 4) << 16 | uint64_t(128 >> 4) << 32 | uint64_t(1) << 46;
 }
+template <bool PAIR>     // a pair's copy runs in both CTAs, each from its own shared memory to its own TMEM
 __device__ __forceinline__ void px_copy_atom(uint32_t taddr, uint64_t d) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+    if constexpr (PAIR) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+    else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+template <bool PAIR>     // a pair's commit arrives on the barrier of both CTAs
+__device__ __forceinline__ void px_commit(uint64_t* bar) {
+    if constexpr (PAIR) umma_commit_pair_both(bar);
+    else umma_commit(bar);
 }
 __device__ __forceinline__ bool px_wait(uint64_t* b, uint32_t parity, volatile int* abort, unsigned long long limit) {
     return mbar_try(b, parity) || mbar_wait(b, parity, abort, limit);
@@ -108,6 +124,12 @@ __device__ __forceinline__ bool px_warp_wait(uint64_t* b, uint32_t parity, volat
 // the whole warp waits, with one outcome
 __device__ __forceinline__ bool px_wait_all(uint64_t* b, uint32_t parity, volatile int* abort, unsigned long long limit) {
     return __all_sync(0xffffffffu, px_wait(b, parity, abort, limit)) != 0;
+}
+// the same on a barrier that the pair's other CTA arrives on too
+template <bool PAIR>
+__device__ __forceinline__ bool px_wait_all_pair(uint64_t* b, uint32_t parity, volatile int* abort, unsigned long long limit) {
+    if constexpr (PAIR) return __all_sync(0xffffffffu, mbar_wait_cluster(b, parity, abort, limit)) != 0;
+    else return px_wait_all(b, parity, abort, limit);
 }
 __device__ __forceinline__ bool px_elect() {
     uint32_t r;
@@ -167,35 +189,39 @@ __device__ __forceinline__ void px_load_scales(const uint8_t* row, int c, int ns
     }
 }
 
-template <bool SWIGLU, int BN>
+template <bool SWIGLU, int BN, bool PAIR>
 __global__ void __launch_bounds__(kPxThreads, 1)
 mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_sw,
                    const __grid_constant__ CUtensorMap tm_a1, const __grid_constant__ CUtensorMap tm_a2,
                    const __grid_constant__ CUtensorMap tm_a4, PxParams p) {
-    using C = PxCfg<BN>;
+    using C = PxCfg<BN, PAIR>;
     constexpr int kSt = C::kStages;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
     uint8_t* sB = sA + kSt * kPxABytes;
     uint8_t* sSf = sB + kSt * C::kBBytes;
-    uint8_t* sEpi = sSf + 2 * C::kSfChunk;
+    uint8_t* sEpi = sSf + kPxSfBufs * C::kSfChunk;
     uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + C::kEpiBytes);
     uint64_t* empty = full + kSt;
     uint64_t* tfull = empty + kSt;
     uint64_t* tempty = tfull + 2;
     uint64_t* sfull = tempty + 2;
-    uint64_t* sempty = sfull + 2;
-    uint64_t* mma_done = sempty + 2;
+    uint64_t* sempty = sfull + kPxSfBufs;
+    uint64_t* mma_done = sempty + kPxSfBufs;
     int* ntile = reinterpret_cast<int*>(mma_done + 1);      // [G + 1] first row tile of each group
     int* off = ntile + kPxGroups + 1;                       // [G + 1] row offsets
     int* wsum = off + kPxGroups + 1;                        // block scan, then the epilogue's wait outcomes
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(wsum + 16);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     volatile int* epi_ok = abort_flag + 1;
+    uint2* table = reinterpret_cast<uint2*>((reinterpret_cast<uintptr_t>(wsum + 24) + 7) & ~uintptr_t(7));
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = p.G;
+    // tiles go to CTAs, or to pairs: the leader (rank 0) issues for both
+    const int rank = PAIR ? int(cluster_ctarank()) : 0;
+    const int first = PAIR ? int(blockIdx.x) >> 1 : int(blockIdx.x), stride = PAIR ? int(gridDim.x) >> 1 : int(gridDim.x);
     // ---- tile list: offsets clamped to [0, R] (a caller's bad table is reported, never followed)
     int nt = 0;
     if (tid < G) {
@@ -221,8 +247,10 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], kPxEpi);
-            mbar_init(&sfull[b], kPxLoaders / 2);
+            mbar_init(&tempty[b], kPxEpi + (PAIR && rank == 0));            // own warps, and for the leader the peer's forwarder
+        }
+        for (int b = 0; b < kPxSfBufs; ++b) {
+            mbar_init(&sfull[b], kPxLoaders / 2 + (PAIR && rank == 0));
             mbar_init(&sempty[b], 1);
         }
         mbar_init(mma_done, 1);
@@ -231,51 +259,89 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(tmem_slot)),
-                     "r"(C::kTmemCols));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        if constexpr (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(tmem_slot)),
+                         "r"(C::kTmemCols));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(tmem_slot)),
+                         "r"(C::kTmemCols));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        }
     }
     __syncthreads();
     if (tid < G) {
         for (int w = 0; w < warp; ++w) inc += wsum[w];
         ntile[tid + 1] = inc;
     }
+    __syncthreads();
+    const int total = ntile[G] * p.m_tiles;
+    // The first kPxTable tiles of this CTA, one thread each: decoding a tile takes a search and two
+    // divisions, some 1800 clocks in each of the roles' loops.
+    if (tid < kPxTable && first + tid * stride < total) {
+        const PxTile tl = px_tile<BN>(first + tid * stride, ntile, off, G, p.m_tiles);
+        table[tid] = make_uint2(uint32_t(tl.row0), uint32_t(tl.nvalid) | uint32_t(tl.g) << 8 | uint32_t(tl.m) << 17);
+    }
+    const auto tile_at = [&](int t, int index) {      // tile t, this CTA's index-th
+        if (index >= kPxTable) return px_tile<BN>(t, ntile, off, G, p.m_tiles);
+        const uint2 e = table[index];
+        return PxTile{int(e.y >> 8 & 511u), int(e.y >> 17), int(e.x), int(e.y & 255u)};
+    };
     tc_fence_before();
     __syncthreads();
+    if constexpr (PAIR) cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int total = ntile[G] * p.m_tiles;
+    // barriers that live in the leader
+    const uint32_t full_lead = PAIR ? mapa_rank(su32(full), 0) : 0u;
+    const uint32_t sfull_lead = PAIR ? mapa_rank(su32(sfull), 0) : 0u;
+    const uint32_t tempty_lead = PAIR ? mapa_rank(su32(tempty), 0) : 0u;
     const int nk = p.nk;
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer (warp-uniform, one elected lane issues)
         const int utotal = __shfl_sync(0xffffffffu, total, 0);
         const bool leader = px_elect();
-        int s = 0, step = 0;
+        int s = 0, step = 0, j = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < utotal && ok; t += gridDim.x) {
-            const PxTile tl = px_tile<BN>(t, ntile, off, G, p.m_tiles);
-            const int g = __shfl_sync(0xffffffffu, tl.g, 0), m = __shfl_sync(0xffffffffu, tl.m, 0);
-            const int row0 = __shfl_sync(0xffffffffu, tl.row0, 0);
+        for (int t = first; t < utotal && ok; t += stride, ++j) {
+            const PxTile tl = tile_at(t, j);
+            const int g = __shfl_sync(0xffffffffu, tl.g, 0);
+            const int m = __shfl_sync(0xffffffffu, PAIR ? 2 * tl.m + rank : tl.m, 0);      // 128-row weight group
+            const int rows = PAIR ? ((tl.nvalid + 15) & ~15) >> 1 : tl.nvalid;                // rows of `a` this CTA loads
+            const int row0 = __shfl_sync(0xffffffffu, tl.row0 + rank * rows, 0);
             const bool shared_grp = g >= p.E;
             const CUtensorMap* mw = shared_grp ? &tm_sw : &tm_w;
             const int wg = shared_grp ? 0 : g;
             // the tile's rows in units of the smallest box, loaded as at most one box of each size
-            const int units = __shfl_sync(0xffffffffu, (tl.nvalid + C::kBox - 1) / C::kBox, 0);
+            const int units = __shfl_sync(0xffffffffu, (rows + C::kBox - 1) / C::kBox, 0);
             const uint32_t bytes = uint32_t(kPxABytes) + uint32_t(units) * (C::kBox * 128u);
             const auto load_w = [&](int kb, int s) {
-                mbar_expect_tx(&full[s], bytes);
                 uint8_t* a = sA + s * kPxABytes;
-                if (SWIGLU) tma_5d(mw, &full[s], a, kb * 128, 0, 0, m * 4, wg);
-                else tma_3d(mw, &full[s], a, kb * 128, m * 128, wg);
+                if constexpr (PAIR) {
+                    // both CTAs' bytes count on the leader's barrier, and only the leader expects them
+                    if (rank == 0) mbar_expect_tx(&full[s], 2 * bytes);
+                    if (SWIGLU) tma_5d_pair(mw, full_lead + 8u * s, a, kb * 128, 0, 0, m * 4, wg);
+                    else tma_3d_pair(mw, full_lead + 8u * s, a, kb * 128, m * 128, wg);
+                } else {
+                    mbar_expect_tx(&full[s], bytes);
+                    if (SWIGLU) tma_5d(mw, &full[s], a, kb * 128, 0, 0, m * 4, wg);
+                    else tma_3d(mw, &full[s], a, kb * 128, m * 128, wg);
+                }
             };
             const auto load_a = [&](int kb, int s) {
                 uint8_t* b = sB + s * C::kBBytes;
                 int r = row0;
-                if (BN > 32 && (units & 4)) { tma_2d(&tm_a4, &full[s], b, kb * 128, r); b += 4 * C::kBox * 128; r += 4 * C::kBox; }
-                if (units & 2) { tma_2d(&tm_a2, &full[s], b, kb * 128, r); b += 2 * C::kBox * 128; r += 2 * C::kBox; }
-                if (units & 1) tma_2d(&tm_a1, &full[s], b, kb * 128, r);
+                const auto box = [&](const CUtensorMap* tm, int n) {
+                    if constexpr (PAIR) tma_2d_pair(tm, full_lead + 8u * s, b, kb * 128, r);
+                    else tma_2d(tm, &full[s], b, kb * 128, r);
+                    b += n * C::kBox * 128;
+                    r += n * C::kBox;
+                };
+                if (BN > 32 && (units & 4)) box(&tm_a4, 4);
+                if (units & 2) box(&tm_a2, 2);
+                if (units & 1) box(&tm_a1, 1);
             };
             int early = 0;                     // stages whose weights are already on their way
             if (step == 0) {
@@ -301,8 +367,10 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
         }
         if (leader) {
             if (!ok) { *abort_flag = 1; atomicExch(p.err, kDevErrTimeout); }
-            for (int st = step > kSt ? step - kSt : 0; st < step; ++st)     // own copies in flight have landed
-                mbar_wait(&full[st % kSt], uint32_t(st / kSt) & 1u, nullptr);
+            // own copies in flight have landed: the leader sees its full barriers complete (in a pair both CTAs'
+            // bytes), the peer that the leader consumed what it copied
+            for (int st = step > kSt ? step - kSt : 0; st < step; ++st)
+                mbar_wait(rank == 0 ? &full[st % kSt] : &empty[st % kSt], uint32_t(st / kSt) & 1u, nullptr);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -311,26 +379,26 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
         // descriptors stay in uniform registers, where the tcgen05 instructions want them.  (Under
         // `if (lane == 0)` every operand is moved there one by one: 1200 clocks a stage of N = 192
         // against under 800.)
-        const int utotal = __shfl_sync(0xffffffffu, total, 0);
+        const int utotal = rank == 0 ? __shfl_sync(0xffffffffu, total, 0) : 0;      // the leader issues for the pair
         const bool leader = px_elect();
         const uint64_t ad0 = sdesc_sw128(su32(sA)), bd0 = sdesc_sw128(su32(sB));
         const uint64_t sf0 = px_atom_desc(su32(sSf));
         int s = 0, j = 0, ch = 0;             // stage, tile and scale chunk counters
         uint32_t phase = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < utotal; t += gridDim.x, ++j) {
-            const PxTile tl = px_tile<BN>(t, ntile, off, G, p.m_tiles);
+        for (int t = first; t < utotal; t += stride, ++j) {
+            const PxTile tl = tile_at(t, j);
             const int N = __shfl_sync(0xffffffffu, (tl.nvalid + 15) & ~15, 0);
             const int buf = j & 1;
-            ok = px_wait_all(&tempty[buf], (uint32_t(j >> 1) & 1u) ^ 1u, abort_flag, p.wait_ns);
+            ok = px_wait_all_pair<PAIR>(&tempty[buf], (uint32_t(j >> 1) & 1u) ^ 1u, abort_flag, p.wait_ns);
             if (!ok) break;
             tc_fence_after();
             const uint32_t dacc = tmem + uint32_t(BN * buf);
-            const uint32_t id0 = idesc_mxf4(N, 0), id2 = idesc_mxf4(N, 2);
+            const uint32_t id0 = idesc_mxf4(PAIR ? 256 : 128, N, 0), id2 = idesc_mxf4(PAIR ? 256 : 128, N, 2);
             const bool two = C::kHalves == 2 && N > 128;
             for (int kb = 0; kb < nk; ++kb) {
                 if ((kb & (kPxChunk - 1)) == 0) {
-                    ok = px_wait_all(&sfull[ch & 1], uint32_t(ch >> 1) & 1u, abort_flag, p.wait_ns);
+                    ok = px_wait_all_pair<PAIR>(&sfull[ch % kPxSfBufs], uint32_t(ch / kPxSfBufs) & 1u, abort_flag, p.wait_ns);
                     if (!ok) break;
                 }
                 ok = px_wait_all(&full[s], phase, abort_flag, p.wait_ns);
@@ -339,12 +407,12 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                 const bool chunk_end = (kb & (kPxChunk - 1)) == kPxChunk - 1 || kb == nk - 1;
                 if (leader) {
                     const uint32_t sfa = tmem + uint32_t(C::kSfBase + (s & 1) * C::kSfCols), sfb = sfa + 8u;
-                    const uint64_t sd = sf0 + uint64_t(((ch & 1) * C::kSfChunk + (kb & (kPxChunk - 1)) * C::kSfBytes) >> 4);
+                    const uint64_t sd = sf0 + uint64_t(((ch % kPxSfBufs) * C::kSfChunk + (kb & (kPxChunk - 1)) * C::kSfBytes) >> 4);
 #pragma unroll
                     for (int a = 0; a < 2; ++a) {
-                        px_copy_atom(sfa + 4u * a, sd + uint64_t(32 * a));
-                        px_copy_atom(sfb + 4u * C::kHalves * a, sd + uint64_t((C::kSfA + a * C::kHalves * 512) >> 4));
-                        if (two) px_copy_atom(sfb + 4u * C::kHalves * a + 4u, sd + uint64_t((C::kSfA + a * C::kHalves * 512 + 512) >> 4));
+                        px_copy_atom<PAIR>(sfa + 4u * a, sd + uint64_t(32 * a));
+                        px_copy_atom<PAIR>(sfb + 4u * C::kHalves * a, sd + uint64_t((C::kSfA + a * C::kHalves * 512) >> 4));
+                        if (two) px_copy_atom<PAIR>(sfb + 4u * C::kHalves * a + 4u, sd + uint64_t((C::kSfA + a * C::kHalves * 512 + 512) >> 4));
                     }
                     const uint64_t ad = ad0 + uint64_t((s * kPxABytes) >> 4), bd = bd0 + uint64_t((s * C::kBBytes) >> 4);
                     const int steps = min(4, (p.K - kb * kPxK) >> 6);       // 64-deep MMAs of this stage
@@ -352,23 +420,42 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                     for (int i = 0; i < 4; ++i) {
                         if (i >= steps) break;
                         const uint32_t hi = (i & 1) ? 2u << 30 : 0u;
-                        umma_mxf4(dacc, ad + uint64_t(2 * i), bd + uint64_t(2 * i), (i & 1) ? id2 : id0,
+                        umma_mxf4<PAIR>(dacc, ad + uint64_t(2 * i), bd + uint64_t(2 * i), (i & 1) ? id2 : id0,
                                   (sfa + 4u * (i >> 1)) | hi, (sfb + 4u * C::kHalves * (i >> 1)) | hi, (kb | i) != 0);
                     }
-                    umma_commit(&empty[s]);
-                    if (chunk_end) umma_commit(&sempty[ch & 1]);
+                    px_commit<PAIR>(&empty[s]);
+                    if (chunk_end) px_commit<PAIR>(&sempty[ch % kPxSfBufs]);
                 }
                 __syncwarp();
                 if (chunk_end) ++ch;
                 if (++s == kSt) { s = 0; phase ^= 1u; }
             }
             if (!ok) break;
-            if (leader) umma_commit(&tfull[buf]);
+            if (leader) px_commit<PAIR>(&tfull[buf]);
             __syncwarp();
         }
+        if (PAIR && rank == 1 && lane < 2) {
+            // The peer's idle issuer passes its CTA's arrivals on to the leader: lane 0 the scale chunks, lane
+            // 1 the accumulators.  (A cluster-scope release takes some 2000 clocks under load; made by the
+            // loader warps themselves it was most of their time.)
+            const int nch = (nk + kPxChunk - 1) / kPxChunk;
+            uint64_t* mine = lane ? tempty : sfull;
+            const uint32_t lead = lane ? tempty_lead : sfull_lead;
+            const int bufs = lane ? 2 : kPxSfBufs;
+            int n = 0, b = 0;
+            uint32_t par = 0;
+            for (int t = first; t < total; t += stride) n += lane ? 1 : nch;
+            for (int e = 0; e < n; ++e) {
+                if (!px_wait(&mine[b], par, abort_flag, p.wait_ns)) { ok = false; break; }
+                mbar_arrive_cluster(lead + 8u * b);
+                if (++b == bufs) { b = 0; par ^= 1u; }
+            }
+            if (!ok) { *abort_flag = 1; atomicExch(p.err, kDevErrTimeout); }
+        }
+        __syncwarp();
         if (leader) {
             if (!ok) { *abort_flag = 1; atomicExch(p.err, kDevErrTimeout); }
-            umma_commit(mma_done);
+            if (rank == 0) px_commit<PAIR>(mma_done);     // completion of every MMA and copy above, in both CTAs
             mbar_wait(mma_done, 0, nullptr);
         }
         __syncwarp();
@@ -385,27 +472,37 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
         const int at = 16 * (i & 31) + 4 * (i >> 5);
         constexpr int kRows = 1 + C::kHalves;
         uint32_t v[kRows][8] = {};
-        int lt = blockIdx.x, lc = 0, cur = -1;      // the load cursor, and the tile its row pointers are of
+        int lt = first, lj = 0, lc = 0, cur = -1;      // the load cursor, and the tile its row pointers are of
         const uint8_t* src[kRows] = {};
         bool take[kRows] = {};
         auto advance = [&](int n) {
-            for (lc += n; lc >= nch; lc -= nch) lt += gridDim.x;
+            for (lc += n; lc >= nch; lc -= nch, ++lj) lt += stride;
+        };
+        const auto weight_row = [&](const PxTile& tl) {      // this thread's A row of a tile
+            const bool shared_grp = tl.g >= p.E;
+            const int mg = PAIR ? 2 * tl.m + rank : tl.m;
+            int wrow;
+            if (SWIGLU) {
+                const int F = p.N >> 1, f = min(mg * 64 + 16 * (i >> 5) + (i & 15), F - 1);
+                wrow = (i & 31) < 16 ? f : F + f;
+            } else {
+                wrow = min(mg * 128 + i, p.N - 1);
+            }
+            return (shared_grp ? p.swsc : p.wsc) + (size_t(shared_grp ? 0 : tl.g) * p.N + wrow) * nsc;
         };
         auto load = [&]() {
             if (lt >= total) return;
             if (lt != cur) {
                 cur = lt;
-                const PxTile tl = px_tile<BN>(lt, ntile, off, G, p.m_tiles);
-                const bool shared_grp = tl.g >= p.E;
-                int wrow;
-                if (SWIGLU) {
-                    const int F = p.N >> 1, f = tl.m * 64 + 16 * (i >> 5) + (i & 15);
-                    wrow = (i & 31) < 16 ? f : F + f;
-                } else {
-                    wrow = min(tl.m * 128 + i, p.N - 1);
-                }
-                src[0] = (shared_grp ? p.swsc : p.wsc) + (size_t(shared_grp ? 0 : tl.g) * p.N + wrow) * nsc;
+                const PxTile tl = tile_at(lt, lj);
+                src[0] = weight_row(tl);
                 take[0] = true;
+                // the next tile's weight scales into L2: behind the code stream a load from DRAM takes
+                // longer than a chunk's MMAs
+                if (grp == 0 && lt + stride < total) {
+                    const uint8_t* nx = weight_row(tile_at(lt + stride, lj + 1));
+                    for (int o = 0; o < nsc; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(nx + o));
+                }
 #pragma unroll
                 for (int h = 0; h < C::kHalves; ++h) {
                     take[1 + h] = i + 128 * h < ((tl.nvalid + 15) & ~15);
@@ -420,9 +517,10 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
         pdl_wait();                            // the activations' scales come from the preceding kernel
         advance(grp);
         load();
-        for (uint32_t n = 0; lt < total; ++n) {
-            if (!px_warp_wait(&sempty[grp], (n & 1u) ^ 1u, abort_flag, p.wait_ns)) { ok = false; break; }
-            uint8_t* d = sSf + grp * C::kSfChunk + at;
+        for (int ch = grp; lt < total; ch += 2) {
+            const int b = ch % kPxSfBufs;
+            if (!px_warp_wait(&sempty[b], (uint32_t(ch / kPxSfBufs) & 1u) ^ 1u, abort_flag, p.wait_ns)) { ok = false; break; }
+            uint8_t* d = sSf + b * C::kSfChunk + at;
 #pragma unroll
             for (int sub = 0; sub < kPxChunk; ++sub)
 #pragma unroll
@@ -434,7 +532,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                 }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sfull[grp]);
+            if (lane == 0) mbar_arrive(&sfull[b]);
             advance(2);
             load();
         }
@@ -447,8 +545,8 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
         const bool lead = warp == 2 + kPxLoaders + 4 * half;
         bool ok = true;
         int j = 0;
-        for (int t = blockIdx.x; t < total; t += gridDim.x, ++j) {
-            const PxTile tl = px_tile<BN>(t, ntile, off, G, p.m_tiles);
+        for (int t = first; t < total; t += stride, ++j) {
+            const PxTile tl = tile_at(t, j);
             const int buf = j & 1;
             const uint32_t par = uint32_t(j >> 1) & 1u;
             if (SWIGLU) {
@@ -466,6 +564,9 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
             }
             if (!ok) break;
             tc_fence_after();
+            const int mg = PAIR ? 2 * tl.m + rank : tl.m;
+            // a pair tile's second weight group may lie past the last one: nothing of it is stored
+            const bool store = !PAIR || mg < (SWIGLU ? p.N / 128 : (p.N + 127) / 128);
             const int nch = (tl.nvalid + 31) >> 5;
             const uint32_t tb = tmem + (uint32_t(q * 32) << 16) + uint32_t(BN * buf);
             for (int c = half; c < nch; c += 2) {
@@ -510,11 +611,11 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                     uint2 cd = make_uint2(e2m1x8(y), e2m1x8(z));
                     if (sc == 255u) cd = make_uint2(0u, 0u);
                     const int n = 32 * c + tok;
-                    if (n < tl.nvalid) {
+                    if (store && n < tl.nvalid) {
                         const int F = p.N >> 1;
                         const size_t row = size_t(tl.row0 + n);
-                        *reinterpret_cast<uint2*>(p.hq + row * (F >> 1) + tl.m * 32 + 8 * part) = cd;
-                        if (!(part & 1)) p.hs[row * (F >> 5) + tl.m * 2 + (part >> 1)] = uint8_t(sc);
+                        *reinterpret_cast<uint2*>(p.hq + row * (F >> 1) + mg * 32 + 8 * part) = cd;
+                        if (!(part & 1)) p.hs[row * (F >> 5) + mg * 2 + (part >> 1)] = uint8_t(sc);
                     }
                     px_bar(1 + half);
                 } else {
@@ -522,7 +623,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
 #pragma unroll
                     for (int i = 0; i < 32; ++i) xb[i * 32 + lane] = f2bf(v[i]);
                     __syncwarp();
-                    const int col = tl.m * 128 + 32 * q;
+                    const int col = mg * 128 + 32 * q;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const int ch = lane + 32 * r, tok = ch >> 2, pp = ch & 3;
@@ -542,34 +643,62 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
         }
         if (!ok) { *abort_flag = 1; if (lane == 0) atomicExch(p.err, kDevErrTimeout); }
     }
+    // a pair: every MMA is complete (mma_done) and both CTAs are past their last TMEM read and remote
+    // arrival before the TMEM is freed and either CTA exits
     tc_fence_before();
     __syncthreads();
+    if constexpr (PAIR) cluster_sync_all();
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols));
+        if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols));
+        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols));
     }
 }
 
-template <bool SWIGLU, int BN>
-static int launch_variant(int grid, bool dependent, cudaStream_t st, const CUtensorMap& tw, const CUtensorMap& tsw,
+template <bool SWIGLU, int BN, bool PAIR>
+static int launch_variant(int64_t tiles, bool dependent, cudaStream_t st, const CUtensorMap& tw, const CUtensorMap& tsw,
                           const CUtensorMap (&ta)[3], const PxParams& p) {
-    constexpr size_t smem = PxCfg<BN>::smem();
+    constexpr size_t smem = PxCfg<BN, PAIR>::smem();
     static PerDeviceOnce attr;
     if (attr([&] {
-            return cudaFuncSetAttribute(mx4_product_kernel<SWIGLU, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+            return cudaFuncSetAttribute(mx4_product_kernel<SWIGLU, BN, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
         }) != cudaSuccess)
         return 2;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kPxThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute at[2];
+    if (PAIR) {
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = 2;
+        at[0].val.clusterDim.y = 1;
+        at[0].val.clusterDim.z = 1;
+        cfg.numAttrs = 1;
+    }
     cfg.attrs = at;
-    cfg.numAttrs = dependent ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, mx4_product_kernel<SWIGLU, BN>, tw, tsw, ta[0], ta[1], ta[2], p) == cudaSuccess ? 0 : 2;
+    int workers = num_sms();       // persistent CTAs, or pairs: as many as fit at once
+    if (PAIR) {
+        static int max_clusters = 0;   // the same on every device of one model: queried once
+        if (!max_clusters) {
+            cfg.gridDim = dim3(2 * (num_sms() / 2));
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, mx4_product_kernel<SWIGLU, BN, PAIR>, &cfg) != cudaSuccess || n <= 0) {
+                cudaGetLastError();
+                n = num_sms() / 2;
+            }
+            max_clusters = n;
+        }
+        workers = max_clusters;
+    }
+    if (tiles < workers) workers = int(tiles);
+    cfg.gridDim = dim3(PAIR ? 2 * workers : workers);
+    if (dependent) {
+        at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+        ++cfg.numAttrs;
+    }
+    return cudaLaunchKernelEx(&cfg, mx4_product_kernel<SWIGLU, BN, PAIR>, tw, tsw, ta[0], ta[1], ta[2], p) == cudaSuccess ? 0 : 2;
 }
 
 int launch_mx4_product(const Mx4Launch& L, cudaStream_t st) {
@@ -581,7 +710,7 @@ int launch_mx4_product(const Mx4Launch& L, cudaStream_t st) {
         if (small && i == 2) { ta[2] = ta[1]; break; }     // BN = 32 has two sizes
         uint64_t dims[2] = {kb, uint64_t(L.R)};
         uint64_t str[1] = {kb};
-        uint32_t box[2] = {128, uint32_t(small ? PxCfg<32>::kBox : PxCfg<224>::kBox) << i};
+        uint32_t box[2] = {128, 16u << i};
         if (!make_map(&ta[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, L.a, 2, dims, str, box)) return 1;
     }
     auto weight_map = [&](CUtensorMap* m, const uint8_t* w, int groups) {
@@ -609,6 +738,7 @@ int launch_mx4_product(const Mx4Launch& L, cudaStream_t st) {
     p.K = L.K;
     p.nk = (L.K + kPxK - 1) / kPxK;
     p.m_tiles = L.swiglu ? L.N / 64 : (L.N + 127) / 128;
+    if (!small) p.m_tiles = (p.m_tiles + 1) / 2;       // a pair takes two 128-row groups
     p.G = L.G; p.E = L.E; p.R = L.R; p.N = wrows;
     p.offsets = L.offsets;
     p.wsc = L.ws; p.swsc = L.sws; p.asc = L.as;
@@ -620,11 +750,12 @@ int launch_mx4_product(const Mx4Launch& L, cudaStream_t st) {
     p.vec = al % 16 == 0 ? 16 : 2;
     const int64_t bn = small ? 32 : 224;
     const int64_t tiles = int64_t(p.m_tiles) * (int64_t(L.G < L.R ? L.G : L.R) + L.R / bn);   // an upper bound
-    const int grid = int(tiles < num_sms() ? tiles : num_sms());
     const bool dep = L.dependent != 0;
     if (L.swiglu)
-        return small ? launch_variant<true, 32>(grid, dep, st, tw, tsw, ta, p) : launch_variant<true, 224>(grid, dep, st, tw, tsw, ta, p);
-    return small ? launch_variant<false, 32>(grid, dep, st, tw, tsw, ta, p) : launch_variant<false, 224>(grid, dep, st, tw, tsw, ta, p);
+        return small ? launch_variant<true, 32, false>(tiles, dep, st, tw, tsw, ta, p)
+                     : launch_variant<true, 224, true>(tiles, dep, st, tw, tsw, ta, p);
+    return small ? launch_variant<false, 32, false>(tiles, dep, st, tw, tsw, ta, p)
+                 : launch_variant<false, 224, true>(tiles, dep, st, tw, tsw, ta, p);
 }
 
 }  // namespace ftmoe
