@@ -111,8 +111,20 @@ __device__ __forceinline__ void px_commit(uint64_t* bar) {
     if constexpr (PAIR) umma_commit_pair_both(bar);
     else umma_commit(bar);
 }
+static __device__ __noinline__ bool px_wait_slow(uint64_t* b, uint32_t parity, volatile int* abort, unsigned long long limit) {
+    const uint64_t t0 = gtimer();
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok) : "r"(su32(b)), "r"(parity), "r"(20000u) : "memory");
+        if (ok) return true;
+        if (abort && *abort) return false;
+        if (gtimer() - t0 > limit) return false;
+    }
+}
 __device__ __forceinline__ bool px_wait(uint64_t* b, uint32_t parity, volatile int* abort, unsigned long long limit) {
-    return mbar_try(b, parity) || mbar_wait(b, parity, abort, limit);
+    return mbar_try(b, parity) || px_wait_slow(b, parity, abort, limit);
 }
 __device__ __forceinline__ bool px_warp_wait(uint64_t* b, uint32_t parity, volatile int* abort, unsigned long long limit) {
     int r = 0;
@@ -250,7 +262,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
             mbar_init(&tempty[b], kPxEpi + (PAIR && rank == 0));            // own warps, and for the leader the peer's forwarder
         }
         for (int b = 0; b < kPxSfBufs; ++b) {
-            mbar_init(&sfull[b], kPxLoaders / 2 + (PAIR && rank == 0));
+            mbar_init(&sfull[b], PAIR ? kPxLoaders : kPxLoaders / 2);      // one group's warps, in a pair of both CTAs
             mbar_init(&sempty[b], 1);
         }
         mbar_init(mma_done, 1);
@@ -434,21 +446,13 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
             if (leader) px_commit<PAIR>(&tfull[buf]);
             __syncwarp();
         }
-        if (PAIR && rank == 1 && lane < 2) {
-            // The peer's idle issuer passes its CTA's arrivals on to the leader: lane 0 the scale chunks, lane
-            // 1 the accumulators.  (A cluster-scope release takes some 2000 clocks under load; made by the
-            // loader warps themselves it was most of their time.)
-            const int nch = (nk + kPxChunk - 1) / kPxChunk;
-            uint64_t* mine = lane ? tempty : sfull;
-            const uint32_t lead = lane ? tempty_lead : sfull_lead;
-            const int bufs = lane ? 2 : kPxSfBufs;
-            int n = 0, b = 0;
-            uint32_t par = 0;
-            for (int t = first; t < total; t += stride) n += lane ? 1 : nch;
-            for (int e = 0; e < n; ++e) {
-                if (!px_wait(&mine[b], par, abort_flag, p.wait_ns)) { ok = false; break; }
-                mbar_arrive_cluster(lead + 8u * b);
-                if (++b == bufs) { b = 0; par ^= 1u; }
+        if (PAIR && rank == 1 && lane == 0) {
+            // The peer's idle issuer passes its epilogue's arrivals on to the leader: one cluster-scope release
+            // per tile (some 2000 clocks under load, behind the epilogue's stores) instead of eight.
+            int j = 0;
+            for (int t = first; t < total; t += stride, ++j) {
+                if (!px_wait(&tempty[j & 1], uint32_t(j >> 1) & 1u, abort_flag, p.wait_ns)) { ok = false; break; }
+                mbar_arrive_cluster(tempty_lead + 8u * (j & 1));
             }
             if (!ok) { *abort_flag = 1; atomicExch(p.err, kDevErrTimeout); }
         }
@@ -532,7 +536,10 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                 }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sfull[b]);
+            if (lane == 0) {
+                if (PAIR && rank == 1) mbar_arrive_cluster(sfull_lead + 8u * b);
+                else mbar_arrive(&sfull[b]);
+            }
             advance(2);
             load();
         }
