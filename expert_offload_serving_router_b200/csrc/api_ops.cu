@@ -27,19 +27,19 @@ static ft_status product_status(int r, const char* what) {
 // region and h's the front of its h region (17/32 of a byte per element against two).
 static ft_status run_experts_mx4(const ft_moe_shape* s, int T, const ft_moe_weights* w, const uint16_t* x,
                                  const int32_t* offsets, const int32_t* inv_pos, uint16_t* o_sorted, const WsLayout& L,
-                                 void* ws, bool dependent, cudaStream_t st) {
+                                 void* ws, cudaStream_t st) {
     const int H = s->hidden, F = s->ffn, E = s->num_experts, S = s->num_shared;
     uint8_t* xq = ws_at<uint8_t>(ws, L.x_sorted);
     uint8_t* xs = xq + size_t(L.R) * (H / 2);
     uint8_t* hq = ws_at<uint8_t>(ws, L.h);
     uint8_t* hs = hq + size_t(L.R) * (F / 2);
-    ft_status r = cuda_ok(launch_mx4_sorted_tokens(T, H, s->top_k, S, x, inv_pos, xq, xs, dependent, st), "token quantisation launch");
+    ft_status r = cuda_ok(launch_mx4_sorted_tokens(T, H, s->top_k, S, x, inv_pos, xq, xs, st), "token quantisation launch");
     if (r) return r;
     Mx4Launch g{};
     g.G = E + S; g.E = E; g.R = L.R;
     g.offsets = offsets;
     g.err = ws_at<uint32_t>(ws, L.err);
-    g.dependent = 1;      // each product overlaps its start (tile list, first weights) with the kernel before it
+    g.early = 1;          // each product overlaps its start (tile list, first weights) with the kernel before it
     g.swiglu = 1; g.N = F; g.K = H;
     g.a = xq; g.as = xs;
     g.w = static_cast<const uint8_t*>(w->w13); g.ws = w->w13_scale;
@@ -143,7 +143,7 @@ ft_status ft_moe_experts_mx4(const ft_moe_shape* shape, int32_t T, const ft_moe_
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if ((s = cuda_state())) return s;
     return run_experts_mx4(shape, T, weights, static_cast<const uint16_t*>(x), offsets, inv_pos,
-                           static_cast<uint16_t*>(o_sorted), L, ws, false, st);
+                           static_cast<uint16_t*>(o_sorted), L, ws, st);
 }
 
 ft_status ft_moe_layer_forward_mx4(const ft_moe_shape* shape, int32_t T, const void* x, const float* w_router,
@@ -179,7 +179,7 @@ ft_status ft_moe_layer_forward_mx4(const ft_moe_shape* shape, int32_t T, const v
                                "permute launch")))
         return s;
     uint16_t* os = ws_at<uint16_t>(ws, L.o_sorted);
-    if ((s = run_experts_mx4(shape, T, weights, xb, po.offsets, inv_pos, os, L, ws, true, st))) return s;
+    if ((s = run_experts_mx4(shape, T, weights, xb, po.offsets, inv_pos, os, L, ws, st))) return s;
     return cuda_ok(launch_combine_dependent(T, H, k, S, L.R, os, inv_pos, gw, static_cast<uint16_t*>(y), st), "combine launch");
 }
 

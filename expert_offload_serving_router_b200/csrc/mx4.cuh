@@ -61,7 +61,7 @@ cudaError_t launch_mx4_quantize(int64_t rows, int cols, int dtype, const void* x
                                 uint8_t* scales, void* values, cudaStream_t st);
 // bf16 rows x [T, H] quantised once and written to their sorted places (inv_pos) of codes / scales
 cudaError_t launch_mx4_sorted_tokens(int T, int H, int k, int S, const uint16_t* x, const int32_t* inv_pos,
-                                     uint8_t* codes, uint8_t* scales, bool dependent, cudaStream_t st);
+                                     uint8_t* codes, uint8_t* scales, cudaStream_t st);
 
 struct Mx4Launch {
     int swiglu;                 // 1: gate/up pairs -> silu(gate) * up -> MXFP4 h; 0: bf16 rows
@@ -77,7 +77,8 @@ struct Mx4Launch {
     uint8_t* hq;                // swiglu == 1: [R, N/2] codes, [R, N/32] scales
     uint8_t* hs;
     uint32_t* err;
-    int dependent;              // launched as the programmatic dependent of the kernel that writes a / as
+    int early;                  // the kernel launched before on the stream is the token quantiser or this product, with
+                                // offsets and weights from before it: they may be read ahead of the wait for it
 };
 // 0 ok, 1 tensor-map failure, 2 launch failure
 int launch_mx4_product(const Mx4Launch& L, cudaStream_t st);

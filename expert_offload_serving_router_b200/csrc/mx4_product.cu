@@ -74,6 +74,7 @@ struct PxParams {
     uint8_t* hs;
     uint32_t* err;
     unsigned long long wait_ns;
+    int early;                // offsets and weights may be read before the wait for the preceding kernel
 };
 
 // kind::mxf4 instruction descriptor: E2M1 x E2M1, both K-major, E8M0 scales, M = 128 (256 for a
@@ -149,6 +150,22 @@ __device__ __forceinline__ bool px_elect() {
     return r != 0;
 }
 __device__ __forceinline__ void px_bar(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+
+// silu(x) = x / (1 + 2^(-x log2 e)) to a few fp32 roundings -- not the tanh approximation of the bf16
+// paths: the E2M1 rounding that follows turns an error near a rounding border into a whole step.  The
+// exponent is carried in two floats (its rounding alone would cost |x| 2^-24), the reciprocal is
+// refined once.  2^88 and more divide to zero; the clamp keeps them out of inf * 0 in the refinement.
+__device__ __forceinline__ float px_silu(float x) {
+    const float n = x * -1.44269502f;                                   // log2 e = 1.44269502 + 1.92596299e-8
+    const float lo = fmaf(x, -1.44269502f, -n) - x * 1.92596299e-8f;
+    float e;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(fminf(n, 120.f)));
+    const float d = 1.f + fmaf(e, lo * 0.693147182f, e);
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(d));
+    r = fmaf(r, fmaf(-d, r, 1.f), r);
+    return x * r;
+}
 
 struct PxTile { int g, m, row0, nvalid; };
 
@@ -234,6 +251,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
     // tiles go to CTAs, or to pairs: the leader (rank 0) issues for both
     const int rank = PAIR ? int(cluster_ctarank()) : 0;
     const int first = PAIR ? int(blockIdx.x) >> 1 : int(blockIdx.x), stride = PAIR ? int(gridDim.x) >> 1 : int(gridDim.x);
+    if (!p.early) pdl_wait();
     // ---- tile list: offsets clamped to [0, R] (a caller's bad table is reported, never followed)
     int nt = 0;
     if (tid < G) {
@@ -598,9 +616,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                         const float recv = __shfl_xor_sync(0xffffffffu, send, 16);
                         const float gt = lo ? v[i] : recv;
                         const float up = lo ? recv : v[16 + i];
-                        // expf, not the tanh approximation of the bf16 paths: the E2M1 rounding that
-                        // follows turns an error near a rounding border into a whole step
-                        hb[(lo ? i : 16 + i) * kPxHRow + fl] = gt / (1.f + expf(-gt)) * up;
+                        hb[(lo ? i : 16 + i) * kPxHRow + fl] = px_silu(gt) * up;
                     }
                     px_bar(1 + half);
                     const int tok = et >> 2, part = et & 3;   // two threads per 32-element block
@@ -663,7 +679,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
 }
 
 template <bool SWIGLU, int BN, bool PAIR>
-static int launch_variant(int64_t tiles, bool dependent, cudaStream_t st, const CUtensorMap& tw, const CUtensorMap& tsw,
+static int launch_variant(int64_t tiles, cudaStream_t st, const CUtensorMap& tw, const CUtensorMap& tsw,
                           const CUtensorMap (&ta)[3], const PxParams& p) {
     constexpr size_t smem = PxCfg<BN, PAIR>::smem();
     static PerDeviceOnce attr;
@@ -700,11 +716,12 @@ static int launch_variant(int64_t tiles, bool dependent, cudaStream_t st, const 
     }
     if (tiles < workers) workers = int(tiles);
     cfg.gridDim = dim3(PAIR ? 2 * workers : workers);
-    if (dependent) {
-        at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
-        ++cfg.numAttrs;
-    }
+    // Always a programmatic dependent.  Behind a kernel of unknown origin everything is read after the
+    // wait; behind the token quantiser or this kernel, which start dependents only after their own
+    // wait and write neither offsets nor weights, those two are final and are read before it (early).
+    at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
     return cudaLaunchKernelEx(&cfg, mx4_product_kernel<SWIGLU, BN, PAIR>, tw, tsw, ta[0], ta[1], ta[2], p) == cudaSuccess ? 0 : 2;
 }
 
@@ -751,18 +768,18 @@ int launch_mx4_product(const Mx4Launch& L, cudaStream_t st) {
     p.wsc = L.ws; p.swsc = L.sws; p.asc = L.as;
     p.out = L.out; p.hq = L.hq; p.hs = L.hs;
     p.err = L.err;
+    p.early = L.early;
     p.wait_ns = gemm_wait_ns();
     const uintptr_t al = reinterpret_cast<uintptr_t>(L.ws) | reinterpret_cast<uintptr_t>(L.as) |
                          (L.G > L.E ? reinterpret_cast<uintptr_t>(L.sws) : 0) | uintptr_t(L.K / 32);
     p.vec = al % 16 == 0 ? 16 : 2;
     const int64_t bn = small ? 32 : 224;
     const int64_t tiles = int64_t(p.m_tiles) * (int64_t(L.G < L.R ? L.G : L.R) + L.R / bn);   // an upper bound
-    const bool dep = L.dependent != 0;
     if (L.swiglu)
-        return small ? launch_variant<true, 32, false>(tiles, dep, st, tw, tsw, ta, p)
-                     : launch_variant<true, 224, true>(tiles, dep, st, tw, tsw, ta, p);
-    return small ? launch_variant<false, 32, false>(tiles, dep, st, tw, tsw, ta, p)
-                 : launch_variant<false, 224, true>(tiles, dep, st, tw, tsw, ta, p);
+        return small ? launch_variant<true, 32, false>(tiles, st, tw, tsw, ta, p)
+                     : launch_variant<true, 224, true>(tiles, st, tw, tsw, ta, p);
+    return small ? launch_variant<false, 32, false>(tiles, st, tw, tsw, ta, p)
+                 : launch_variant<false, 224, true>(tiles, st, tw, tsw, ta, p);
 }
 
 }  // namespace ftmoe

@@ -155,44 +155,60 @@ cudaError_t launch_mx4_quantize(int64_t rows, int cols, int dtype, const void* x
 
 // Tokens into sorted order: each row of x is read and quantised once and its codes are written to
 // the k (+ 1 shared) sorted places of the token's pairs, so a batch costs one read of x and R rows
-// of 17/32 bytes per element written (a gather of bf16 rows writes 2 bytes per element).
+// of 17/32 bytes per element written (a gather of bf16 rows writes 2 bytes per element).  A thread
+// takes a whole 32-element block, so a place costs one 16-byte store and the scale byte (with eight
+// elements per thread, four 4-byte stores: 2049 x 2816, nine places, PX_SORTED_OLD -> PX_SORTED_NEW).
 // A position outside [0, R) (a dropped pair) is skipped.
-__global__ void __launch_bounds__(kQThreads) mx4_sorted_tokens_kernel(int T, int nv, int k, int S,
+__global__ void __launch_bounds__(kQThreads) mx4_sorted_tokens_kernel(int T, int nb, int k, int S,
                                                                       const uint16_t* __restrict__ x,
                                                                       const int32_t* __restrict__ inv_pos,
-                                                                      uint32_t* __restrict__ codes,
+                                                                      uint4* __restrict__ codes,
                                                                       uint8_t* __restrict__ scales) {
     const int R = T * k + S * T;
-    const int64_t total = int64_t(T) * nv;
+    const int64_t total = int64_t(T) * nb;
     const int64_t at = int64_t(blockIdx.x) * kQThreads + threadIdx.x;
-    const int64_t id = at < total ? at : 0;
-    const int t = int(id <= 0xFFFFFFFFll ? int64_t(uint32_t(id) / uint32_t(nv)) : id / nv);
-    const int c = int(id - int64_t(t) * nv);
     pdl_wait();
     pdl_trigger();      // after the wait: the permutation is final for the product that follows
-    const uint4 u[1] = {ldg_nc_v4(reinterpret_cast<const uint4*>(x) + id)};
+    if (at >= total) return;
+    const int t = int(at <= 0xFFFFFFFFll ? int64_t(uint32_t(at) / uint32_t(nb)) : at / nb);
+    const int c = int(at - int64_t(t) * nb);
+    uint4 u[4][1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i][0] = ldg_nc_v4(reinterpret_cast<const uint4*>(x) + at * 4 + i);
     int pos[kMaxTopK + 1];
 #pragma unroll
-    for (int j = 0; j < kMaxTopK; ++j) pos[j] = j < k ? inv_pos[t * k + j] : -1;
-    pos[kMaxTopK] = S ? inv_pos[T * k + t] : -1;
-    float v[8];
-    Elem<__nv_bfloat16>::unpack(u, v);
-    uint32_t s;
-    const uint32_t q = mx4_quad(v, s);
-    if (at >= total) return;
+    for (int j = 0; j < kMaxTopK; ++j) pos[j] = j < k ? inv_pos[int64_t(t) * k + j] : -1;
+    pos[kMaxTopK] = S ? inv_pos[int64_t(T) * k + t] : -1;
+    float v[4][8];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        Elem<__nv_bfloat16>::unpack(u[i], v[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[i][j]) & 0x7FFFFFFFu);
+    }
+    float mul;
+    const uint32_t s = mx4_scale_of(m, mul);
+    uint32_t q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] *= mul;
+        q[i] = s == 255u ? 0u : e2m1x8(v[i]);
+    }
 #pragma unroll
     for (int j = 0; j < kMaxTopK + 1; ++j) {
         if (pos[j] < 0 || pos[j] >= R) continue;
-        codes[size_t(pos[j]) * nv + c] = q;
-        if ((c & 3) == 0) scales[size_t(pos[j]) * (nv / 4) + (c >> 2)] = uint8_t(s);
+        codes[size_t(pos[j]) * nb + c] = make_uint4(q[0], q[1], q[2], q[3]);
+        scales[size_t(pos[j]) * nb + c] = uint8_t(s);
     }
 }
 
 cudaError_t launch_mx4_sorted_tokens(int T, int H, int k, int S, const uint16_t* x, const int32_t* inv_pos,
-                                     uint8_t* codes, uint8_t* scales, bool dependent, cudaStream_t st) {
+                                     uint8_t* codes, uint8_t* scales, cudaStream_t st) {
     if (T <= 0) return cudaSuccess;
-    const int nv = H / 8;
-    const int64_t blocks = (int64_t(T) * nv + kQThreads - 1) / kQThreads;
+    const int nb = H / 32;
+    const int64_t blocks = (int64_t(T) * nb + kQThreads - 1) / kQThreads;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(blocks));
     cfg.blockDim = dim3(kQThreads);
@@ -201,8 +217,8 @@ cudaError_t launch_mx4_sorted_tokens(int T, int H, int k, int S, const uint16_t*
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = dependent ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, mx4_sorted_tokens_kernel, T, nv, k, S, x, inv_pos, reinterpret_cast<uint32_t*>(codes), scales);
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, mx4_sorted_tokens_kernel, T, nb, k, S, x, inv_pos, reinterpret_cast<uint4*>(codes), scales);
 }
 
 }  // namespace ftmoe
