@@ -254,7 +254,7 @@ ft_status ft_moe_route_backward(const ft_moe_shape* shape, int32_t T, const void
     if ((s = cuda_state())) return s;
     return cuda_ok(launch_route_backward(T, shape->hidden, shape->top_k, shape->num_experts, static_cast<const uint16_t*>(x),
                                          topk_idx, topk_w, d_topk_w, offsets, sorted_flat, dlogits, dw_router, dbias,
-                                         ws_at<float>(ws, L.x_sorted), st),
+                                         ws_at<uint8_t>(ws, L.x_sorted), st),
                    "route backward launch");
 }
 

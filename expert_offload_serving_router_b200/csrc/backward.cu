@@ -6,6 +6,7 @@
 //   permute:   dx[t] = bf16(sum_j dxs[pos(t,j)] (+ dxs[pos_shared(t)]) (+ sum_j dl[t,j] * Wr[e(t,j)]))
 //   route:     s = sum_j g_j d_g_j,  dl_j = g_j (d_g_j - s);  dWr[e] = sum over e's pairs of dl * x[t],
 //              db[e] = sum of dl   (the logits that were not kept have gradient zero)
+#include "decode_common.cuh"
 #include "kernels.h"
 
 namespace ftmoe {
@@ -148,16 +149,32 @@ __global__ void __launch_bounds__(256) permute_backward_kernel(int T, int nv, in
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
     if (ROUTER) {
+        // four rows of W_r in flight (with a load, its sums, then the next: 38 us for 4096 x 2048, k = 8)
+        int e[kMaxTopK];
+        float d[kMaxTopK];
 #pragma unroll
         for (int j = 0; j < kMaxTopK; ++j) {
-            if (j >= k) break;
-            const int e = idx[int64_t(t) * k + j];
-            if (e < 0 || e >= E) continue;
-            const float d = dl[int64_t(t) * k + j];
-            const float4* w = reinterpret_cast<const float4*>(wr) + (int64_t(e) * nv + c) * 2;
-            const float4 a = __ldg(w), b = __ldg(w + 1);
-            acc[0] = fmaf(d, a.x, acc[0]); acc[1] = fmaf(d, a.y, acc[1]); acc[2] = fmaf(d, a.z, acc[2]); acc[3] = fmaf(d, a.w, acc[3]);
-            acc[4] = fmaf(d, b.x, acc[4]); acc[5] = fmaf(d, b.y, acc[5]); acc[6] = fmaf(d, b.z, acc[6]); acc[7] = fmaf(d, b.w, acc[7]);
+            e[j] = j < k ? idx[int64_t(t) * k + j] : -1;
+            d[j] = j < k ? dl[int64_t(t) * k + j] : 0.f;
+        }
+#pragma unroll
+        for (int j0 = 0; j0 < kMaxTopK; j0 += 4) {
+            float4 w[4][2];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int ej = e[j0 + j];
+                const float4* row = reinterpret_cast<const float4*>(wr) + (int64_t(ej) * nv + c) * 2;
+                const bool ok = ej >= 0 && ej < E;
+                w[j][0] = ok ? __ldg(row) : make_float4(0.f, 0.f, 0.f, 0.f);
+                w[j][1] = ok ? __ldg(row + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float dj = d[j0 + j];
+                const float4 a = w[j][0], b = w[j][1];
+                acc[0] = fmaf(dj, a.x, acc[0]); acc[1] = fmaf(dj, a.y, acc[1]); acc[2] = fmaf(dj, a.z, acc[2]); acc[3] = fmaf(dj, a.w, acc[3]);
+                acc[4] = fmaf(dj, b.x, acc[4]); acc[5] = fmaf(dj, b.y, acc[5]); acc[6] = fmaf(dj, b.z, acc[6]); acc[7] = fmaf(dj, b.w, acc[7]);
+            }
         }
     }
 #pragma unroll
@@ -181,15 +198,6 @@ cudaError_t launch_permute_backward(int T, int H, int k, int S, int E, int R, co
 }
 
 // ------------------------------------------------------------------ router
-// The sorted order makes dWr a segmented sum over consecutive rows.  Segments are fixed runs of
-// `seg` sorted rows; a CTA sums one segment for 1024 columns, expert by expert.  An expert that
-// lies inside one segment is written directly; one that crosses a segment border leaves a partial
-// sum per segment -- slot 2s (the rows at the segment's start) or 2s + 1 (the rows at its end) --
-// and route_backward_join_kernel adds them in segment order.
-constexpr int kRbThreads = 128;
-constexpr int kRbCols = kRbThreads * 8;
-constexpr int kRbMaxSeg = 64;
-
 struct RouteBackward {
     int T, H, k, E, P, seg, nseg;
     const uint16_t* x;
@@ -201,7 +209,8 @@ struct RouteBackward {
     float* dlogits;
     float* dw;       // [E, H] or NULL
     float* db;       // [E] or NULL
-    float* part;     // [2 nseg, H]
+    uint4* meta;     // [P] sorted rows: token, dlogit, expert
+    float* part;     // [2 nseg, H] partial sums of experts that cross a segment border
     float* part_b;   // [2 nseg]
 };
 
@@ -212,26 +221,113 @@ __device__ __forceinline__ float dlogit_of(const RouteBackward& a, int p) {
     for (int j = 0; j < a.k; ++j) s = fmaf(a.gw[t0 + j], a.dgw[t0 + j], s);
     return a.gw[p] * (a.dgw[p] - s);
 }
+__device__ __forceinline__ int routed_rows(const RouteBackward& a) { return max(0, min(a.offsets[a.E], a.P)); }
+
+// Small batches (P <= kRbSmall), one launch: CTA (expert, 256 columns), the expert's rows dealt to
+// eight warps, their sums joined through shared memory in warp order.  CTA e also writes the e-th
+// share of dlogits.
+constexpr int kRbSmall = 1024;
+
+__global__ void __launch_bounds__(256) route_backward_small_kernel(RouteBackward a) {
+    __shared__ float s_dl[256];
+    __shared__ int s_tok[256];
+    __shared__ float s_sum[8][256];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, e = blockIdx.x;
+    if (blockIdx.y == 0) {
+        const int share = (a.P + a.E - 1) / a.E;
+        for (int i = tid; i < share; i += 256)
+            if (e * share + i < a.P) a.dlogits[e * share + i] = dlogit_of(a, e * share + i);
+    }
+    if (!a.dw && !a.db) return;
+    const int rows = routed_rows(a);
+    const int lo = max(0, min(a.offsets[e], rows)), hi = max(lo, min(a.offsets[e + 1], rows));
+    const int col = blockIdx.y * 256 + lane * 8;
+    const bool in = a.dw && col < a.H;
+    float acc[8], accb = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+    for (int base = lo; base < hi; base += 256) {
+        const int n = min(256, hi - base);
+        __syncthreads();
+        if (tid < n) {
+            const int flat = a.sorted_flat[base + tid];
+            const bool ok = flat >= 0 && flat < a.P;
+            s_tok[tid] = ok ? flat / a.k : 0;
+            s_dl[tid] = ok ? dlogit_of(a, flat) : 0.f;
+        }
+        __syncthreads();
+        for (int r = warp; r < n; r += 32) {
+            uint4 u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                u[i] = in && r + 8 * i < n ? ldg_nc_v4(a.x + int64_t(s_tok[r + 8 * i]) * a.H + col) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (r + 8 * i >= n) break;
+                const float d = s_dl[r + 8 * i];
+                float f[8];
+                unpack8(u[i], f);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) acc[c] = fmaf(d, f[c], acc[c]);
+                accb += d;
+            }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) s_sum[warp][lane * 8 + c] = acc[c];
+    __syncthreads();
+    if (a.dw && blockIdx.y * 256 + tid < a.H) {
+        float s = s_sum[0][tid];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) s += s_sum[w][tid];
+        a.dw[int64_t(e) * a.H + blockIdx.y * 256 + tid] = s;
+    }
+    if (a.db && blockIdx.y == 0) {
+        __syncthreads();
+        if (lane == 0) s_sum[0][warp] = accb;
+        __syncthreads();
+        if (tid == 0) {
+            float s = 0.f;
+            for (int w = 0; w < 8; ++w) s += s_sum[0][w];
+            a.db[e] = s;
+        }
+    }
+}
+
+// Larger batches: the sorted order makes dWr a segmented sum over consecutive rows.  Segments are
+// fixed runs of `seg` sorted rows; a CTA sums one segment for 1024 columns, expert by expert.  An
+// expert that lies inside one segment is written directly; one that crosses a border leaves a partial
+// sum per segment -- slot 2s (the rows at the segment's start) or 2s + 1 (the rows at its end) -- and
+// the join adds them in segment order.
+// Bound by L2: each of the k rows of a token is read again (8192 x 4096, k = 6: 403 MB).  Keeping a
+// chunk's 64-column slice of x in shared memory reads x once, but walks rows of 128 bytes, and was
+// bound by instructions (117 us with FMAs, 119 us with mma.m16n8k16 over a three-plane split, for the
+// case that takes 60 us here).
+__global__ void __launch_bounds__(256) route_backward_prep_kernel(RouteBackward a) {
+    pdl_trigger();         // the kernel after this one reads nothing before its wait
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i >= a.P) return;
+    a.dlogits[i] = dlogit_of(a, i);
+    if ((!a.dw && !a.db) || i >= routed_rows(a)) return;
+    const int flat = a.sorted_flat[i];
+    const bool ok = flat >= 0 && flat < a.P;
+    const int e = ok ? a.idx[flat] : -1;
+    a.meta[i] = make_uint4(uint32_t(ok ? flat / a.k : 0), __float_as_uint(ok ? dlogit_of(a, flat) : 0.f),
+                           uint32_t(e < a.E ? e : -1), 0u);
+}
+
+constexpr int kRbThreads = 128;
+constexpr int kRbCols = kRbThreads * 8;
+constexpr int kRbMaxSeg = 64;
 
 __global__ void __launch_bounds__(kRbThreads) route_backward_kernel(RouteBackward a) {
-    __shared__ float s_dl[kRbMaxSeg];
-    __shared__ int s_tok[kRbMaxSeg];
-    __shared__ int s_e[kRbMaxSeg];
-    const int tid = threadIdx.x, sg = blockIdx.x;
-    const int r0 = sg * a.seg;
-    const int rows = max(0, min(a.offsets ? a.offsets[a.E] : 0, a.P));   // routed rows
-    const int n = max(0, min(a.seg, rows - r0));
-    if (blockIdx.y == 0 && tid < a.seg && r0 + tid < a.P) a.dlogits[r0 + tid] = dlogit_of(a, r0 + tid);
-    if (!a.dw && !a.db) return;
-    if (tid < n) {
-        const int flat = a.sorted_flat[r0 + tid];
-        const bool ok = flat >= 0 && flat < a.P;
-        int e = ok ? a.idx[flat] : -1;
-        if (e >= a.E) e = -1;
-        s_e[tid] = e;
-        s_tok[tid] = ok ? flat / a.k : 0;
-        s_dl[tid] = ok ? dlogit_of(a, flat) : 0.f;
-    }
+    __shared__ uint4 s_m[kRbMaxSeg + 1];
+    const int tid = threadIdx.x, sg = blockIdx.x, r0 = sg * a.seg;
+    pdl_wait();
+    pdl_trigger();
+    const int n = max(0, min(a.seg, routed_rows(a) - r0));
+    if (tid < n) s_m[tid] = a.meta[r0 + tid];
+    if (tid == n) s_m[tid] = make_uint4(0u, 0u, 0xFFFFFFFEu, 0u);     // no row's expert: ends the last run
     __syncthreads();
     const int col = blockIdx.y * kRbCols + tid * 8;
     const bool in = a.dw && col < a.H;
@@ -243,19 +339,19 @@ __global__ void __launch_bounds__(kRbThreads) route_backward_kernel(RouteBackwar
         uint4 u[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            u[i] = in && b + i < n ? ldg_nc_v4(a.x + int64_t(s_tok[b + i]) * a.H + col) : make_uint4(0, 0, 0, 0);
+            u[i] = in && b + i < n ? ldg_nc_v4(a.x + int64_t(s_m[b + i].x) * a.H + col) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int r = b + i;
             if (r >= n) break;
-            const float d = s_dl[r];
+            const float d = __uint_as_float(s_m[r].y);
             float f[8];
             unpack8(u[i], f);
 #pragma unroll
             for (int c = 0; c < 8; ++c) acc[c] = fmaf(d, f[c], acc[c]);
             accb += d;
-            const int e = s_e[r];
-            if (r + 1 == n || s_e[r + 1] != e) {          // the run of this expert's rows ends here
+            const int e = int(s_m[r].z);
+            if (int(s_m[r + 1].z) != e) {                  // the run of this expert's rows ends here
                 if (e >= 0) {
                     const bool whole = r0 + run0 == a.offsets[e] && r0 + r + 1 == a.offsets[e + 1];
                     const int slot = 2 * sg + (run0 ? 1 : 0);
@@ -275,59 +371,89 @@ __global__ void __launch_bounds__(kRbThreads) route_backward_kernel(RouteBackwar
     }
 }
 
-// experts without rows get zeros; experts of several segments the sum of their partial sums
+// Experts without rows get zeros, experts of several segments the sum of their partial sums: CTA
+// (expert, 128 columns), the slots dealt to eight warps, joined in warp order.
 __global__ void __launch_bounds__(256) route_backward_join_kernel(RouteBackward a) {
-    const int e = blockIdx.x;
+    __shared__ float4 s_sum[8][32];
+    __shared__ float s_b[8];
+    const int e = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_wait();
     const int lo = a.offsets[e], hi = a.offsets[e + 1];
     const bool none = hi <= lo || lo < 0 || hi > a.P;
-    const int s0 = none ? 0 : lo / a.seg, s1 = none ? 0 : (hi - 1) / a.seg;
+    const int s0 = none ? 0 : lo / a.seg, s1 = none ? -1 : (hi - 1) / a.seg;
     if (!none && s0 == s1) return;
-    const int col = (blockIdx.y * 256 + threadIdx.x) * 4;
-    const int first = 2 * s0 + (lo % a.seg ? 1 : 0);
-    if (a.dw && col < a.H) {
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (!none) {
-            s = *reinterpret_cast<const float4*>(a.part + int64_t(first) * a.H + col);
+    const int col = blockIdx.y * 128 + lane * 4;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sb = 0.f;
 #pragma unroll 4
-            for (int g = s0 + 1; g <= s1; ++g) {
-                const float4 v = *reinterpret_cast<const float4*>(a.part + int64_t(2 * g) * a.H + col);
-                s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-            }
+    for (int g = s0 + warp; g <= s1; g += 8) {
+        const int slot = 2 * g + (g == s0 && lo % a.seg ? 1 : 0);
+        if (a.dw) {
+            const float4 v = *reinterpret_cast<const float4*>(a.part + int64_t(slot) * a.H + col);
+            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
         }
-        *reinterpret_cast<float4*>(a.dw + int64_t(e) * a.H + col) = s;
+        if (a.db) sb += a.part_b[slot];
     }
-    if (a.db && blockIdx.y == 0 && threadIdx.x == 0) {
-        float s = 0.f;
-        if (!none) {
-            s = a.part_b[first];
-            for (int g = s0 + 1; g <= s1; ++g) s += a.part_b[2 * g];
-        }
-        a.db[e] = s;
+    s_sum[warp][lane] = s;
+    if (lane == 0) s_b[warp] = sb;
+    __syncthreads();
+    if (warp) return;
+#pragma unroll
+    for (int w = 1; w < 8; ++w) {
+        const float4 v = s_sum[w][lane];
+        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+        sb += s_b[w];
     }
+    if (a.dw) *reinterpret_cast<float4*>(a.dw + int64_t(e) * a.H + col) = s;
+    if (a.db && blockIdx.y == 0 && lane == 0) a.db[e] = sb;
+}
+
+// rows per segment: short ones until they fill the SMs, then longer ones (fewer partial sums)
+static int route_segment(int P) { return P <= 16384 ? 16 : kRbMaxSeg; }
+
+// scratch at `part`, as laid out below; nothing for small batches
+size_t route_backward_part_bytes(int T, int H, int k) {
+    const int64_t P = int64_t(T) * k;
+    if (P <= kRbSmall) return 0;
+    const int64_t nseg = (P + route_segment(int(P)) - 1) / route_segment(int(P));
+    return size_t(P) * 16 + size_t(2) * nseg * (size_t(H) + 1) * 4;
 }
 
 cudaError_t launch_route_backward(int T, int H, int k, int E, const uint16_t* x, const int32_t* idx, const float* gw,
                                   const float* dgw, const int32_t* offsets, const int32_t* sorted_flat, float* dlogits,
-                                  float* dw, float* db, float* part, cudaStream_t st) {
+                                  float* dw, float* db, void* part, cudaStream_t st) {
     RouteBackward a{};
     a.T = T; a.H = H; a.k = k; a.E = E; a.P = T * k;
-    // short segments until they fill the SMs, then longer ones (fewer partial sums)
-    a.seg = a.P <= 16384 ? 16 : kRbMaxSeg;
-    a.nseg = (a.P + a.seg - 1) / a.seg;
     a.x = x; a.idx = idx; a.gw = gw; a.dgw = dgw;
     a.offsets = offsets; a.sorted_flat = sorted_flat;
     a.dlogits = dlogits; a.dw = dw; a.db = db;
-    a.part = part;
-    a.part_b = part + int64_t(2) * a.nseg * H;
-    const int cols = dw ? (H + kRbCols - 1) / kRbCols : 1;
-    route_backward_kernel<<<dim3(a.nseg, cols), kRbThreads, 0, st>>>(a);
-    if (dw || db) route_backward_join_kernel<<<dim3(E, dw ? (H + 1023) / 1024 : 1), 256, 0, st>>>(a);
+    if (a.P <= kRbSmall) {
+        route_backward_small_kernel<<<dim3(E, dw ? (H + 255) / 256 : 1), 256, 0, st>>>(a);
+        return cudaGetLastError();
+    }
+    a.seg = route_segment(a.P);
+    a.nseg = (a.P + a.seg - 1) / a.seg;
+    a.meta = static_cast<uint4*>(part);
+    a.part = reinterpret_cast<float*>(a.meta + a.P);
+    a.part_b = a.part + int64_t(2) * a.nseg * H;
+    route_backward_prep_kernel<<<(a.P + 255) / 256, 256, 0, st>>>(a);
+    if (dw || db) {
+        cudaLaunchConfig_t cfg{};          // both start while the kernel before them drains
+        cfg.gridDim = dim3(a.nseg, dw ? (H + kRbCols - 1) / kRbCols : 1);
+        cfg.blockDim = dim3(kRbThreads);
+        cfg.stream = st;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        cudaError_t e = cudaLaunchKernelEx(&cfg, route_backward_kernel, a);
+        if (e != cudaSuccess) return e;
+        cfg.gridDim = dim3(E, dw ? H / 128 : 1);
+        cfg.blockDim = dim3(256);
+        return cudaLaunchKernelEx(&cfg, route_backward_join_kernel, a);
+    }
     return cudaGetLastError();
-}
-
-size_t route_backward_part_bytes(int T, int H, int k) {
-    const int P = T * k, seg = P <= 16384 ? 16 : kRbMaxSeg, nseg = (P + seg - 1) / seg;
-    return nseg > 1 ? size_t(2) * nseg * (size_t(H) + 1) * sizeof(float) : 0;
 }
 
 }  // namespace ftmoe

@@ -115,7 +115,7 @@ cudaError_t launch_permute_backward(int T, int H, int k, int S, int E, int R, co
                                     const int32_t* idx, const float* dl, const float* wr, uint16_t* dx, cudaStream_t st);
 cudaError_t launch_route_backward(int T, int H, int k, int E, const uint16_t* x, const int32_t* idx, const float* gw,
                                   const float* dgw, const int32_t* offsets, const int32_t* sorted_flat, float* dlogits,
-                                  float* dw, float* db, float* part, cudaStream_t st);
+                                  float* dw, float* db, void* part, cudaStream_t st);
 size_t route_backward_part_bytes(int T, int H, int k);   // partial sums at `part`
 cudaError_t launch_unit_rms(int T, int H, const uint16_t* in, uint16_t* out, float eps, cudaStream_t st);
 

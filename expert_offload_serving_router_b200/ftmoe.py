@@ -130,10 +130,12 @@ def header_functions() -> list[str]:
 def _p(t):
     if t is None:
         return None
+    try:
+        return t.data_ptr()
+    except AttributeError:
+        pass
     if isinstance(t, int):
         return t
-    if hasattr(t, "data_ptr"):
-        return t.data_ptr()
     if isinstance(t, ctypes.Array):
         return ctypes.addressof(t)
     raise TypeError(f"cannot pass {type(t)} as a pointer")
