@@ -38,7 +38,7 @@ constexpr int kPxSfBufs = 4;                 // chunk buffers
 constexpr int kPxABytes = 128 * 128;
 constexpr int kPxGroups = kMaxExperts + 1;
 constexpr int kPxTable = 256;                // tiles of a CTA (pair) worked out ahead
-constexpr int kPxHRow = 65;                  // fp32 per token row of the h buffer: 64 + 1 against bank conflicts
+constexpr int kPxHRow = 36;                  // fp32 per token row of an h buffer: 32 + 4 against bank conflicts
 
 template <int BN, bool PAIR>
 struct PxCfg {
@@ -52,7 +52,7 @@ struct PxCfg {
     static constexpr int kSfCols = 2 * 4 + 2 * 4 * kHalves;        // TMEM columns of one stage's scales
     static constexpr int kSfBase = 2 * BN;                         // after the two accumulators
     static constexpr int kTmemCols = BN == 32 ? 128 : 512;
-    static constexpr int kEpiBytes = 2 * 32 * kPxHRow * 4;         // >= 8 x 2 KB transpose buffers
+    static constexpr int kEpiBytes = 4 * 32 * kPxHRow * 4;         // four h buffers; >= 8 x 2 KB transpose buffers
     static constexpr size_t smem() {
         return 1024 + size_t(kStages) * (kPxABytes + kBBytes) + kPxSfBufs * kSfChunk + kEpiBytes + (2 * kStages + 2 * kPxSfBufs + 8) * 8 +
                (2 * (kPxGroups + 1) + 32) * 4 + kPxTable * 8;
@@ -149,7 +149,15 @@ __device__ __forceinline__ bool px_elect() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
     return r != 0;
 }
-__device__ __forceinline__ void px_bar(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void px_bar(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+// 16 TMEM lanes x 32 columns as mma fragments: v[4 k + i] = lane (lane / 4 + 8 (i / 2)), column 8 k + 2 (lane % 4) + i % 2
+__device__ __forceinline__ void px_ld_frag(uint32_t taddr, float (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(taddr));
+}
 
 // silu(x) = x / (1 + 2^(-x log2 e)) to a few fp32 roundings -- not the tanh approximation of the bf16
 // paths: the E2M1 rounding that follows turns an error near a rounding border into a whole step.  The
@@ -241,10 +249,10 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
     int* ntile = reinterpret_cast<int*>(mma_done + 1);      // [G + 1] first row tile of each group
     int* off = ntile + kPxGroups + 1;                       // [G + 1] row offsets
     int* wsum = off + kPxGroups + 1;                        // block scan, then the epilogue's wait outcomes
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(wsum + 16);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(wsum + 20);   // 18 warps' sums before it
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    volatile int* epi_ok = abort_flag + 1;
-    uint2* table = reinterpret_cast<uint2*>((reinterpret_cast<uintptr_t>(wsum + 24) + 7) & ~uintptr_t(7));
+    volatile int* epi_ok = abort_flag + 1;                          // [4 pairs of warps][tile parity]
+    uint2* table = reinterpret_cast<uint2*>((reinterpret_cast<uintptr_t>(wsum + 30) + 7) & ~uintptr_t(7));
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = p.G;
@@ -566,8 +574,8 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
         // ------------------------------------------------ epilogue
         const int q = warp & 3;                       // TMEM lanes 32q .. 32q + 31
         const int half = (warp - 2 - kPxLoaders) >> 2;   // column chunks half, half + 2, ...
-        const int et = tid - 32 * (2 + kPxLoaders) - 128 * half;   // 0..127 within the half
-        const bool lead = warp == 2 + kPxLoaders + 4 * half;
+        // SwiGLU: the two warps of a lane half of the accumulator share the 32 columns of h of one MXFP4 block
+        const int duo = 2 * half + (q >> 1), et = 32 * (q & 1) + lane;      // pair 0..3, thread 0..63 of it
         bool ok = true;
         int j = 0;
         for (int t = first; t < total; t += stride, ++j) {
@@ -575,15 +583,14 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
             const int buf = j & 1;
             const uint32_t par = uint32_t(j >> 1) & 1u;
             if (SWIGLU) {
-                // the half's four warps meet at barriers below, so they take one common outcome
-                if (lead) {
+                // the two warps meet at barriers below, so they take one common outcome
+                if (!(q & 1)) {
                     const bool r = px_warp_wait(&tfull[buf], par, abort_flag, p.wait_ns);
-                    if (lane == 0) epi_ok[half] = r;
+                    if (lane == 0) epi_ok[2 * duo + buf] = r;
                     __threadfence_block();
                 }
-                px_bar(1 + half);
-                ok = epi_ok[half] != 0;
-                px_bar(1 + half);
+                px_bar(1 + duo);
+                ok = epi_ok[2 * duo + buf] != 0;       // overwritten two tiles on, past the next tile's barrier
             } else {
                 ok = px_warp_wait(&tfull[buf], par, abort_flag, p.wait_ns);
             }
@@ -595,36 +602,36 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
             const int nch = (tl.nvalid + 31) >> 5;
             const uint32_t tb = tmem + (uint32_t(q * 32) << 16) + uint32_t(BN * buf);
             for (int c = half; c < nch; c += 2) {
-                float v[32];
-                tmem_ld32_nowait(tb + uint32_t(32 * c), v);
-                tmem_wait_16(v);
-                tmem_fence_regs(v + 16);
+                float v0[16], v1[16];                  // the warp's first and second 16 weight rows
+                px_ld_frag(tb + uint32_t(32 * c), v0);
+                px_ld_frag(tb + (16u << 16) + uint32_t(32 * c), v1);
+                tmem_wait_16(v0);
+                tmem_fence_regs(v1);
                 if (c + 2 >= nch) {                    // this warp's last read of the accumulator
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&tempty[buf]);
                 }
                 if constexpr (SWIGLU) {
-                    // lanes 0-15 hold gate rows f, lanes 16-31 the matching up rows: halves swap so that
-                    // each lane finishes 16 tokens of its f, staged as fp32 [token][64 f]
-                    float* hb = reinterpret_cast<float*>(sEpi) + half * 32 * kPxHRow;
-                    const int fl = 16 * q + (lane & 15);
-                    const bool lo = lane < 16;
+                    // the first 16 rows are gate rows f, the second the up rows of the same f: both in the same
+                    // place of the fragment.  h is staged as fp32 [token][32 f of the pair]
+                    float* hb = reinterpret_cast<float*>(sEpi) + duo * 32 * kPxHRow;
+                    float* hw = hb + (lane & 3) * 2 * kPxHRow + 16 * (q & 1) + (lane >> 2);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float send = lo ? v[16 + i] : v[i];
-                        const float recv = __shfl_xor_sync(0xffffffffu, send, 16);
-                        const float gt = lo ? v[i] : recv;
-                        const float up = lo ? recv : v[16 + i];
-                        hb[(lo ? i : 16 + i) * kPxHRow + fl] = px_silu(gt) * up;
-                    }
-                    px_bar(1 + half);
-                    const int tok = et >> 2, part = et & 3;   // two threads per 32-element block
-                    const float* hr = hb + tok * kPxHRow + 16 * part;
+                    for (int i = 0; i < 16; ++i)
+                        hw[(8 * (i >> 2) + (i & 1)) * kPxHRow + 8 * ((i >> 1) & 1)] = px_silu(v0[i]) * v1[i];
+                    px_bar(1 + duo);
+                    const int tok = et >> 1, part = et & 1;   // two threads per 32-element block
+                    const float4* hr = reinterpret_cast<const float4*>(hb + tok * kPxHRow + 16 * part);
                     float x[16];
                     uint32_t m = 0;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) { x[i] = hr[i]; m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu); }
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 u = hr[i];
+                        x[4 * i] = u.x; x[4 * i + 1] = u.y; x[4 * i + 2] = u.z; x[4 * i + 3] = u.w;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
                     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
                     float mul;
                     const uint32_t sc = mx4_scale_of(m, mul);
@@ -637,14 +644,22 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                     if (store && n < tl.nvalid) {
                         const int F = p.N >> 1;
                         const size_t row = size_t(tl.row0 + n);
-                        *reinterpret_cast<uint2*>(p.hq + row * (F >> 1) + mg * 32 + 8 * part) = cd;
-                        if (!(part & 1)) p.hs[row * (F >> 5) + mg * 2 + (part >> 1)] = uint8_t(sc);
+                        *reinterpret_cast<uint2*>(p.hq + row * (F >> 1) + mg * 32 + 16 * (q >> 1) + 8 * part) = cd;
+                        if (!part) p.hs[row * (F >> 5) + mg * 2 + (q >> 1)] = uint8_t(sc);
                     }
-                    px_bar(1 + half);
+                    px_bar(1 + duo);
                 } else {
-                    uint16_t* xb = reinterpret_cast<uint16_t*>(sEpi + (warp - 2 - kPxLoaders) * kXposeBytes);
+                    // bf16 pairs of two tokens per weight row, stored transposed: token rows of 64 bytes, their
+                    // 16-byte pieces XORed with the token so that neither side meets on a bank
+                    uint8_t* xb = sEpi + (warp - 2 - kPxLoaders) * kXposeBytes;
+                    const uint32_t dst = su32(xb) + uint32_t(lane & 7) * 64u + uint32_t(((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) xb[i * 32 + lane] = f2bf(v[i]);
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t a0 = pack_bf16x2(v0[4 * k], v0[4 * k + 1]), a1 = pack_bf16x2(v0[4 * k + 2], v0[4 * k + 3]);
+                        const uint32_t a2 = pack_bf16x2(v1[4 * k], v1[4 * k + 1]), a3 = pack_bf16x2(v1[4 * k + 2], v1[4 * k + 3]);
+                        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
+                                     ::"r"(dst + 512u * k), "r"(a0), "r"(a1), "r"(a2), "r"(a3) : "memory");
+                    }
                     __syncwarp();
                     const int col = mg * 128 + 32 * q;
 #pragma unroll
@@ -653,7 +668,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                         const int n = 32 * c + tok;
                         if (n < tl.nvalid && col + 8 * pp < p.N)
                             *reinterpret_cast<uint4*>(p.out + size_t(tl.row0 + n) * p.N + col + 8 * pp) =
-                                *reinterpret_cast<const uint4*>(xb + tok * 32 + 8 * pp);
+                                *reinterpret_cast<const uint4*>(xb + tok * 64 + ((pp ^ ((tok >> 1) & 3)) << 4));
                     }
                     __syncwarp();
                 }

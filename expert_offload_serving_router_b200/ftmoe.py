@@ -146,9 +146,7 @@ def _s(stream):
         import torch
         # the handle alone, without building a Stream object (3 us a call, more than a kernel launch)
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is None or not torch.cuda.is_initialized():
-            return torch.cuda.current_stream().cuda_stream
-        return raw(torch.cuda.current_device())
+        return torch.cuda.current_stream().cuda_stream if raw is None else raw(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
