@@ -26,6 +26,7 @@
 #include "decode_common.cuh"
 #include "gemm_common.cuh"
 #include "mx4.cuh"
+#include <cmath>
 
 namespace ftmoe {
 
@@ -42,16 +43,16 @@ constexpr int kPxHRow = 36;                  // fp32 per token row of an h buffe
 
 template <int BN, bool PAIR>
 struct PxCfg {
-    static constexpr int kStages = BN == 32 ? 8 : PAIR ? 5 : 3;
+    static constexpr int kStages = BN == 32 ? 8 : BN == 96 ? 6 : 5;
     static constexpr int kHalves = BN > 128 ? 2 : 1;               // 128-row scale atoms of B per 128-deep K step
     static constexpr int kBBytes = (PAIR ? BN / 2 : BN) * 128;     // a pair's CTA loads half of the rows
-    static constexpr int kBox = BN == 32 || PAIR ? 16 : 32;                // rows of the smallest activation box; the others are 2x, 4x
+    static constexpr int kBox = BN == 96 ? 32 : 16;                // rows of the smallest activation box; the others are 2x, 4x
     static constexpr int kSfA = 2 * 512;
     static constexpr int kSfBytes = kSfA + 2 * kHalves * 512;      // scale atoms of one stage
     static constexpr int kSfChunk = kPxChunk * kSfBytes;           // of one chunk
     static constexpr int kSfCols = 2 * 4 + 2 * 4 * kHalves;        // TMEM columns of one stage's scales
     static constexpr int kSfBase = 2 * BN;                         // after the two accumulators
-    static constexpr int kTmemCols = BN == 32 ? 128 : 512;
+    static constexpr int kTmemCols = BN == 32 ? 128 : BN == 96 ? 256 : 512;
     static constexpr int kEpiBytes = 4 * 32 * kPxHRow * 4;         // four h buffers; >= 8 x 2 KB transpose buffers
     static constexpr size_t smem() {
         return 1024 + size_t(kStages) * (kPxABytes + kBBytes) + kPxSfBufs * kSfChunk + kEpiBytes + (2 * kStages + 2 * kPxSfBufs + 8) * 8 +
@@ -740,16 +741,40 @@ static int launch_variant(int64_t tiles, cudaStream_t st, const CUtensorMap& tw,
     return cudaLaunchKernelEx(&cfg, mx4_product_kernel<SWIGLU, BN, PAIR>, tw, tsw, ta[0], ta[1], ta[2], p) == cudaSuccess ? 0 : 2;
 }
 
+// Which tile: the persistent workers (CTAs, or pairs) take rounds of tiles, so the estimate is rounds
+// times the measured time of a round, 6.5 : 8 : 12 for the three tiles (K = 4096, one round of each:
+// 9.9, 11.2 and 14.7 us).  Row tiles of a group: one while its average is well inside the tile, else as
+// many as the bound allows.  Measured (us, BN = 32 / 96 / pairs; the pick is the smallest but for the
+// first, where all three are within 7 %):
+//   256 groups x 24 rows, 4096 x 4096: 386 / 379 / 406;   x 48: 691 / 404 / 425;   x 192: - / - / 550
+//   129 groups x 143 rows, 1408 x 2816: 189 / 93 / 71;    one group, 4096 x 4096: 64 rows 9.9 / 10.3 / 12.7,
+//   200 rows 16.2 / 11.2 / 14.7, 800 rows 40 / 18 / 16;   1000 rows, 256 x 4096: 9.9 / 11.6 / 14.5
+static int pick_tile(const Mx4Launch& L, int row_groups) {
+    const double groups = L.G < L.R ? L.G : L.R, avg = L.R / groups;
+    const int bn[3] = {32, 96, 224};
+    const double cost[3] = {6.5, 8., 12.};
+    int best = 0;
+    double least = 0.;
+    for (int i = 0; i < 3; ++i) {
+        const double tiles = groups * (avg <= 0.8 * bn[i] ? 1. : 1. + avg / bn[i]) * (i == 2 ? (row_groups + 1) / 2 : row_groups);
+        const double t = cost[i] * ceil(tiles / (i == 2 ? num_sms() / 2 : num_sms()));
+        if (i == 0 || t < least) { best = i; least = t; }
+    }
+    return best;
+}
+
 int launch_mx4_product(const Mx4Launch& L, cudaStream_t st) {
     const int wrows = L.swiglu ? 2 * L.N : L.N;        // weight rows per group
     const uint64_t kb = uint64_t(L.K) / 2;             // code bytes per row
-    const bool small = L.R <= 16 * L.G;
+    const int row_groups = L.swiglu ? L.N / 64 : (L.N + 127) / 128;      // 128-row weight groups
+    const int tile = pick_tile(L, row_groups);
+    const bool small = tile == 0, mid = tile == 1;
     CUtensorMap tw{}, tsw{}, ta[3]{};
     for (int i = 0; i < 3; ++i) {
-        if (small && i == 2) { ta[2] = ta[1]; break; }     // BN = 32 has two sizes
+        if ((small || mid) && i == 2) { ta[2] = ta[1]; break; }     // BN = 32 and 96 have two sizes
         uint64_t dims[2] = {kb, uint64_t(L.R)};
         uint64_t str[1] = {kb};
-        uint32_t box[2] = {128, 16u << i};
+        uint32_t box[2] = {128, (mid ? 32u : 16u) << i};
         if (!make_map(&ta[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, L.a, 2, dims, str, box)) return 1;
     }
     auto weight_map = [&](CUtensorMap* m, const uint8_t* w, int groups) {
@@ -776,8 +801,7 @@ int launch_mx4_product(const Mx4Launch& L, cudaStream_t st) {
     PxParams p{};
     p.K = L.K;
     p.nk = (L.K + kPxK - 1) / kPxK;
-    p.m_tiles = L.swiglu ? L.N / 64 : (L.N + 127) / 128;
-    if (!small) p.m_tiles = (p.m_tiles + 1) / 2;       // a pair takes two 128-row groups
+    p.m_tiles = tile == 2 ? (row_groups + 1) / 2 : row_groups;           // a pair takes two
     p.G = L.G; p.E = L.E; p.R = L.R; p.N = wrows;
     p.offsets = L.offsets;
     p.wsc = L.ws; p.swsc = L.sws; p.asc = L.as;
@@ -788,12 +812,14 @@ int launch_mx4_product(const Mx4Launch& L, cudaStream_t st) {
     const uintptr_t al = reinterpret_cast<uintptr_t>(L.ws) | reinterpret_cast<uintptr_t>(L.as) |
                          (L.G > L.E ? reinterpret_cast<uintptr_t>(L.sws) : 0) | uintptr_t(L.K / 32);
     p.vec = al % 16 == 0 ? 16 : 2;
-    const int64_t bn = small ? 32 : 224;
+    const int64_t bn = small ? 32 : mid ? 96 : 224;
     const int64_t tiles = int64_t(p.m_tiles) * (int64_t(L.G < L.R ? L.G : L.R) + L.R / bn);   // an upper bound
     if (L.swiglu)
         return small ? launch_variant<true, 32, false>(tiles, st, tw, tsw, ta, p)
+               : mid ? launch_variant<true, 96, false>(tiles, st, tw, tsw, ta, p)
                      : launch_variant<true, 224, true>(tiles, st, tw, tsw, ta, p);
     return small ? launch_variant<false, 32, false>(tiles, st, tw, tsw, ta, p)
+           : mid ? launch_variant<false, 96, false>(tiles, st, tw, tsw, ta, p)
                  : launch_variant<false, 224, true>(tiles, st, tw, tsw, ta, p);
 }
 
