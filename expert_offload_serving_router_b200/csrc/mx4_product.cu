@@ -13,16 +13,23 @@
 // rows costs an N = 16 MMA.  Tiles are (group, at most BN rows, 128 weight rows); a group of n rows
 // is cut into ceil(n / BN) nearly equal pieces.  The tile list is built by every CTA from the group
 // offsets (a block scan), so nothing but the offsets has to come from the caller.
-//   BN = 224: two accumulators of 224 columns and two sets of scale columns fill the 512 TMEM
-//             columns; 4 stages of 47 KB.
-//   BN = 32:  few rows per group (decode batches): 8 stages of 22 KB keep more weight bytes in flight.
+//   BN = 32:   decode batches: 8 stages of 20 KB keep 128 KB of weights in flight per SM.  Bound by HBM
+//              (256 groups, 12 rows each, 4096 x 4096: 361 us, 6.3 TB/s).
+//   BN = 96:   a few dozen rows a group: 6 stages of 28 KB (48 rows each: 394 us, 5.9 TB/s).
+//   BN = 224:  long prompts, on CTA pairs (cta_group::2, M = 256): each CTA loads 128 weight rows and half
+//              of the tile's rows of `a`, 5 stages of 30 KB; two accumulators of 224 columns and two sets
+//              of scale columns fill the 512 TMEM columns.  One CTA per tile moves 40 KB per 256-deep
+//              stage and SM and ran at 580-600 us where pairs take 550 (256 groups x 192 rows, 4096 x 4096:
+//              2.8 GB, 1.65 PFLOP; clocks fall to ~1.4 GHz under the power cap).
 //
 // Roles of the persistent CTA: warp 0 TMA producer (codes of both operands, 256-deep K stages, 128-byte
-// swizzle); warp 1 TMEM allocator and MMA issuer; warps 2-5 read the row-major scale bytes and lay them
+// swizzle); warp 1 TMEM allocator and MMA issuer; warps 2-9 read the row-major scale bytes and lay them
 // out as tcgen05.cp source atoms (32 x 16 bytes per 128 rows and 128-deep K step: byte 16 (row % 32) +
-// 4 (row / 32) + j = row's scale of the step's block j); warps 6-13 epilogue, two per TMEM lane quarter.
-// The MMA thread copies a stage's atoms into TMEM right before the stage's MMAs (copies and MMAs of one
-// thread complete in issue order).  Every wait is bounded.
+// 4 (row / 32) + j = row's scale of the step's block j); warps 10-17 epilogue, two per TMEM lane quarter.
+// The MMA warp copies a stage's atoms into TMEM right before the stage's MMAs (copies and MMAs of one
+// thread complete in issue order).  Alone on an SM a stage of N = 192 costs 417 clocks (the MMAs 384,
+// the six copies hide behind them); beside the other roles it is about twice that.
+// Every wait is bounded.
 #include "decode_common.cuh"
 #include "gemm_common.cuh"
 #include "mx4.cuh"
@@ -113,7 +120,9 @@ __device__ __forceinline__ void px_commit(uint64_t* bar) {
     if constexpr (PAIR) umma_commit_pair_both(bar);
     else umma_commit(bar);
 }
+// the bounded wait with polls that may sleep 20 us each (a shortened bound is polled without)
 static __device__ __noinline__ bool px_wait_slow(uint64_t* b, uint32_t parity, volatile int* abort, unsigned long long limit) {
+    if (limit < kWaitNs) return mbar_wait(b, parity, abort, limit);
     const uint64_t t0 = gtimer();
     for (;;) {
         uint32_t ok;
@@ -394,7 +403,8 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                 __syncwarp();
             }
             for (int kb = 0; kb < nk; ++kb, ++step) {
-                ok = px_wait_all(&empty[s], phase ^ 1u, abort_flag, p.wait_ns);
+                // a stage of the first round is free, and its weights may be on their way: it is always completed
+                ok = kb < early || px_wait_all(&empty[s], phase ^ 1u, abort_flag, p.wait_ns);
                 if (!ok) break;
                 if (leader) {
                     if (kb >= early) load_w(kb, s);
@@ -408,8 +418,9 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
             if (!ok) { *abort_flag = 1; atomicExch(p.err, kDevErrTimeout); }
             // own copies in flight have landed: the leader sees its full barriers complete (in a pair both CTAs'
             // bytes), the peer that the leader consumed what it copied
+            // (after an abort the other CTA may never bring its part: one default bound is ample for one's own)
             for (int st = step > kSt ? step - kSt : 0; st < step; ++st)
-                mbar_wait(rank == 0 ? &full[st % kSt] : &empty[st % kSt], uint32_t(st / kSt) & 1u, nullptr);
+                if (!mbar_wait(rank == 0 ? &full[st % kSt] : &empty[st % kSt], uint32_t(st / kSt) & 1u, nullptr)) break;
         }
         __syncwarp();
     } else if (warp == 1) {

@@ -142,7 +142,10 @@ def activations(g, rows, k):
 @pytest.mark.parametrize("groups,rows,n,k,skew", [
     (1, 1, 128, 64, 0), (1, 1, 8, 64, 0), (1, 3, 24, 128, 0), (1, 33, 136, 192, 0), (1, 224, 128, 256, 0),
     (1, 225, 256, 512, 0), (1, 700, 384, 704, 0), (2, 449, 128, 320, 0), (5, 97, 200, 768, 1.5), (8, 300, 128, 1024, 2),
-    (8, 1, 640, 2816, 0), (256, 6, 256, 4096, 0), (256, 300, 128, 2048, 1), (256, 5000, 64, 256, 1), (3, 2500, 128, 8192, 0)])
+    (8, 1, 640, 2816, 0), (256, 6, 256, 4096, 0), (256, 300, 128, 2048, 1), (256, 5000, 64, 256, 1), (3, 2500, 128, 8192, 0),
+    # the 96-row tile and the pairs (odd counts of 128-row groups, ragged K, a group of one row among large ones)
+    (16, 640, 1536, 320, 0), (9, 700, 2056, 768, 1), (1, 1999, 2176, 320, 0), (1, 4100, 2184, 1088, 0), (64, 6400, 2048, 192, 0.3),
+    (5, 4500, 1160, 704, 2.5)])
 def test_product(groups, rows, n, k, skew):
     g = np.random.default_rng(groups * 1000 + rows + n + k)
     off = M.random_offsets(g, groups, rows, skew)
@@ -327,7 +330,8 @@ def experts64(w, off, tok, x, E, Fd, H):
 
 @pytest.mark.parametrize("T,H,Fd,E,k,S", [(1, 128, 64, 1, 1, 0), (1, 256, 128, 8, 2, 1), (5, 512, 192, 16, 3, 0),
                                           (40, 384, 64, 8, 8, 1), (33, 1024, 704, 4, 2, 0), (300, 256, 128, 4, 2, 1),
-                                          (700, 128, 320, 3, 1, 0), (64, 2816, 64, 128, 8, 1)])
+                                          (700, 128, 320, 3, 1, 0), (64, 2816, 64, 128, 8, 1), (301, 128, 704, 32, 8, 1),
+                                          (640, 256, 704, 32, 6, 1), (2000, 128, 1984, 4, 2, 0)])
 def test_experts_mx4(T, H, Fd, E, k, S):
     import torch
     import oracle  # noqa: F401
@@ -447,3 +451,82 @@ def test_quantized_weights_run_the_layer():
     rel = ((y16.double() - first.double()).norm() / y16.double().norm()).item()
     # x and h each carry at most a quarter of their block's largest element as error; in the norm well under 1/2
     assert rel < 0.5
+
+
+@pytest.mark.parametrize("groups,rows,n,k", [(256, 40, 1024, 2048), (16, 640, 1536, 2048), (8, 3000, 2048, 2048)])
+def test_product_wait_timeout_is_reported_and_the_next_call_is_exact(groups, rows, n, k):
+    """A bound shorter than any stage: the kernel gives up, reports it, and leaves the context usable."""
+    import torch
+    g = np.random.default_rng(31)
+    off = M.random_offsets(g, groups, rows)
+    ac, asc = activations(g, rows, k)
+    wc, ws_ = M.random_weights(g, groups, n, k)
+    base = run_product(off, ac, asc, wc, ws_, n, k)
+    args = [cuda(off), cuda(ac), cuda(asc), cuda(wc), cuda(ws_)]
+    ws = new_ws()
+    out = torch.empty(rows, n, dtype=torch.bfloat16, device="cuda")
+    prev = F.ft_set_pipeline_wait_limit_ns(1)
+    try:
+        F.ft_mx4_product(groups, rows, n, k, *args, out, ws)
+        with pytest.raises(F.FtError) as ei:
+            F.ft_moe_check(ws)
+    finally:
+        F.ft_set_pipeline_wait_limit_ns(prev)
+    assert ei.value.status == F.FT_ERR_DEVICE_CHECK and "timed out" in str(ei.value)
+    F.ft_mx4_product(groups, rows, n, k, *args, out, ws)
+    F.ft_moe_check(ws)
+    assert np.array_equal(out.double().cpu().numpy(), base)
+
+
+def test_experts_mx4_wait_timeout_is_reported_and_the_next_call_is_exact():
+    import torch
+    g = np.random.default_rng(32)
+    T, H, Fd, E, k, S = 640, 512, 704, 32, 6, 1
+    idx, off, sf, inv = routing(g, T, E, k, S)
+    w, d, weights = layer_weights(g, E, S, H, Fd)
+    x = torch.from_numpy(g.standard_normal((T, H))).to(torch.bfloat16).cuda()
+    shape = F.make_shape(H, Fd, E, k, S, F.FT_W_MXFP4)
+    ws = new_ws(F.ft_moe_workspace_bytes(shape, T))
+    off, inv = cuda(off), cuda(inv)
+    outs = []
+    for limit in (0, 1, 0):
+        o = torch.empty(T * (k + S), H, dtype=torch.bfloat16, device="cuda")
+        prev = F.ft_set_pipeline_wait_limit_ns(limit)
+        try:
+            F.ft_moe_experts_mx4(shape, T, weights, x, off, inv, o, ws)
+            if limit:
+                with pytest.raises(F.FtError) as ei:
+                    F.ft_moe_check(ws)
+                assert ei.value.status == F.FT_ERR_DEVICE_CHECK
+            else:
+                F.ft_moe_check(ws)
+        finally:
+            F.ft_set_pipeline_wait_limit_ns(prev)
+        outs.append(o)
+    assert torch.equal(outs[0].view(torch.int16), outs[2].view(torch.int16))
+
+
+def test_two_layers_on_two_streams_with_a_workspace_each():
+    import torch
+    g = np.random.default_rng(33)
+    T, H, Fd, E, k = 200, 512, 256, 16, 4
+    shape = F.make_shape(H, Fd, E, k, 0, F.FT_W_MXFP4)
+    runs = []
+    for i in range(2):
+        w, d, weights = layer_weights(g, E, 0, H, Fd)
+        x = torch.from_numpy(g.standard_normal((T, H))).to(torch.bfloat16).cuda()
+        wr = torch.from_numpy(g.standard_normal((E, H)).astype(np.float32) * 0.02).cuda()
+        ws = new_ws(F.ft_moe_workspace_bytes(shape, T))
+        y = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+        F.ft_moe_layer_forward_mx4(shape, T, x, wr, None, weights, y, None, None, ws)
+        F.ft_moe_check(ws)
+        runs.append((x, wr, weights, ws, y, y.clone(), d))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for st, (x, wr, weights, ws, y, want, d) in zip(streams, runs):
+            F.ft_moe_layer_forward_mx4(shape, T, x, wr, None, weights, y, None, None, ws, stream=st)
+    torch.cuda.synchronize()
+    for x, wr, weights, ws, y, want, d in runs:
+        F.ft_moe_check(ws)
+        assert torch.equal(y.view(torch.int16), want.view(torch.int16))
