@@ -270,16 +270,18 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
     const int rank = PAIR ? int(cluster_ctarank()) : 0;
     const int first = PAIR ? int(blockIdx.x) >> 1 : int(blockIdx.x), stride = PAIR ? int(gridDim.x) >> 1 : int(gridDim.x);
     if (!p.early) pdl_wait();
-    // ---- tile list: offsets clamped to [0, R] (a caller's bad table is reported, never followed)
-    int nt = 0;
+    // ---- tile list.  A table that is not ascending in [0, R] is reported and nothing of it followed.
+    int nt = 0, bad = 0;
     if (tid < G) {
-        const int lo0 = p.offsets[tid], hi0 = p.offsets[tid + 1];
-        const int lo = min(max(lo0, 0), p.R), hi = min(max(hi0, lo), p.R);
-        if ((lo != lo0 || hi != hi0) && blockIdx.x == 0) atomicExch(p.err, kDevErrOffsets);
+        const int lo = p.offsets[tid], hi = p.offsets[tid + 1];
+        bad = lo < 0 || hi < lo || hi > p.R;
         off[tid] = lo;
-        // a group's end is the next group's clamped start; the two only differ in a table already reported
-        nt = (max(min(max(hi0, 0), p.R) - lo, 0) + BN - 1) / BN;
         if (tid == G - 1) off[G] = hi;
+        nt = (hi - lo + BN - 1) / BN;
+    }
+    if (__syncthreads_or(bad)) {
+        if (bad && blockIdx.x == 0) atomicExch(p.err, kDevErrOffsets);
+        nt = 0;
     }
     int inc = nt;
 #pragma unroll
@@ -693,6 +695,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
         }
         if (!ok) { *abort_flag = 1; if (lane == 0) atomicExch(p.err, kDevErrTimeout); }
     }
+    if (warp == 0) pdl_wait();     // a CTA without tiles too: the grid's end stands for all before it
     // a pair: every MMA is complete (mma_done) and both CTAs are past their last TMEM read and remote
     // arrival before the TMEM is freed and either CTA exits
     tc_fence_before();

@@ -141,15 +141,39 @@ def _p(t):
     raise TypeError(f"cannot pass {type(t)} as a pointer")
 
 
+_torch = None
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
 def _s(stream):
     if stream is None:
-        import torch
+        torch = _torch or _load_torch()
         # the handle alone, without building a Stream object (3 us a call, more than a kernel launch)
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         return torch.cuda.current_stream().cuda_stream if raw is None else raw(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _here(*tensors):
+    """The launch goes to the current device: a tensor that lives elsewhere is an error, not an access there."""
+    dev = None
+    for t in tensors:
+        try:
+            d = t.get_device()
+        except AttributeError:      # an address or None
+            continue
+        if dev is None:
+            dev = (_torch or _load_torch()).cuda.current_device()
+        if d != dev:
+            raise FtError(FT_ERR_INVALID_ARG, f"a tensor is on {t.device}, but device {dev} is current")
 
 
 def _check(st: int):
@@ -270,6 +294,7 @@ def ft_moe_unit_rms(T, H, x_in, x_out, eps=1e-6, stream=None):
 
 
 def ft_mx4_quantize(rows, cols, dtype, x, x_stride, codes, scales, values=None, stream=None):
+    _here(x, codes, scales, values)
     _check(lib().ft_mx4_quantize(rows, cols, dtype, _p(x), x_stride, _p(codes), _p(scales), _p(values), _s(stream)))
 
 
@@ -278,34 +303,40 @@ def ft_mx4_product_workspace_bytes(groups, rows, n, k) -> int:
 
 
 def ft_mx4_product(groups, rows, n, k, offsets, a_codes, a_scales, w_codes, w_scales, out, ws, ws_bytes=None, stream=None):
+    _here(offsets, a_codes, a_scales, w_codes, w_scales, out, ws)
     _check(lib().ft_mx4_product(groups, rows, n, k, _p(offsets), _p(a_codes), _p(a_scales), _p(w_codes), _p(w_scales),
                                 _p(out), _p(ws), _nbytes(ws, ws_bytes), _s(stream)))
 
 
 def ft_moe_experts_mx4(shape, T, weights, x, offsets, inv_pos, o_sorted, ws, ws_bytes=None, stream=None):
+    _here(x, offsets, inv_pos, o_sorted, ws)
     _check(lib().ft_moe_experts_mx4(ctypes.byref(shape), T, ctypes.byref(weights), _p(x), _p(offsets), _p(inv_pos),
                                     _p(o_sorted), _p(ws), _nbytes(ws, ws_bytes), _s(stream)))
 
 
 def ft_moe_layer_forward_mx4(shape, T, x, w_router, bias, weights, y, topk_idx_out, logits_out, ws, ws_bytes=None,
                              stream=None):
+    _here(x, w_router, bias, y, topk_idx_out, logits_out, ws)
     _check(lib().ft_moe_layer_forward_mx4(ctypes.byref(shape), T, _p(x), _p(w_router), _p(bias), ctypes.byref(weights),
                                           _p(y), _p(topk_idx_out), _p(logits_out), _p(ws), _nbytes(ws, ws_bytes),
                                           _s(stream)))
 
 
 def ft_moe_combine_backward(shape, T, dy, o_sorted, inv_pos, topk_w, d_o_sorted, d_topk_w, stream=None):
+    _here(dy, o_sorted, inv_pos, topk_w, d_o_sorted, d_topk_w)
     _check(lib().ft_moe_combine_backward(ctypes.byref(shape), T, _p(dy), _p(o_sorted), _p(inv_pos), _p(topk_w),
                                          _p(d_o_sorted), _p(d_topk_w), _s(stream)))
 
 
 def ft_moe_permute_backward(shape, T, dx_sorted, inv_pos, topk_idx, dlogits, w_router, dx, stream=None):
+    _here(dx_sorted, inv_pos, topk_idx, dlogits, w_router, dx)
     _check(lib().ft_moe_permute_backward(ctypes.byref(shape), T, _p(dx_sorted), _p(inv_pos), _p(topk_idx), _p(dlogits),
                                          _p(w_router), _p(dx), _s(stream)))
 
 
 def ft_moe_route_backward(shape, T, x, topk_idx, topk_w, d_topk_w, offsets, sorted_flat, dlogits, dw_router, dbias, ws,
                           ws_bytes=None, stream=None):
+    _here(x, topk_idx, topk_w, d_topk_w, offsets, sorted_flat, dlogits, dw_router, dbias, ws)
     _check(lib().ft_moe_route_backward(ctypes.byref(shape), T, _p(x), _p(topk_idx), _p(topk_w), _p(d_topk_w), _p(offsets),
                                        _p(sorted_flat), _p(dlogits), _p(dw_router), _p(dbias), _p(ws),
                                        _nbytes(ws, ws_bytes), _s(stream)))

@@ -165,7 +165,7 @@ int32_t ft_set_block_scaled_decode(int32_t mode);
 int32_t ft_moe_decode_kernels(const ft_moe_shape* shape, int32_t T);
 
 /* Bound on every pipeline wait of the grouped-GEMM kernels (steps 3 and 4 when
- * T > decode threshold): the time, in ns, a role waits for a stage without
+ * T > decode threshold, and the MXFP4 x MXFP4 product): the time, in ns, a role waits for a stage without
  * progress before it gives up.  Default 4 s (4000000000); ns = 0 restores the
  * default.  Process-wide, applies to launches enqueued after the call; returns
  * the previous bound.  A wait that runs out makes the kernel give up cleanly:
@@ -189,7 +189,8 @@ ft_status ft_moe_workspace_init(void* ws, size_t ws_bytes, void* stream);
 
 /* Synchronises `stream`, then reads and clears the device status word of ws.
  * FT_ERR_DEVICE_CHECK if a kernel since the last check saw a routed expert id
- * outside [0,E) or gave up a bounded wait (tcgen05 pipeline timeout);
+ * outside [0,E) or group offsets out of order, or gave up a bounded wait (tcgen05
+ * pipeline timeout);
  * FT_ERR_CUDA on an asynchronous CUDA error.  This is the only synchronising
  * call of the layer API. */
 ft_status ft_moe_check(void* ws, void* stream);
@@ -285,8 +286,8 @@ ft_status ft_moe_unit_rms(int32_t T, int32_t H, const void* in, void* out, float
  * codes: all its values read as NaN, and so does every product with it.
  * In products, the codes and scales are multiplied exactly (tcgen05 kind::mxf4, block-scaled)
  * and summed in fp32.  Carrying the activations in 4 bits costs accuracy that the bf16
- * paths keep (each activation is within 2^-2 of its value relative to the block's largest
- * element's power of two); which form a layer runs is the caller's choice of entry point.
+ * paths keep (an element moves by up to a quarter of its block's largest magnitude); which
+ * form a layer runs is the caller's choice of entry point.
  * ------------------------------------------------------------------------- */
 
 /* Quantises rows.  x: device [rows, cols] of `dtype` (ft_dtype) with x_stride elements from one
@@ -307,9 +308,8 @@ size_t ft_mx4_product_workspace_bytes(int32_t groups, int32_t rows, int32_t n, i
  * [offsets[g], offsets[g+1]) of each group g (groups == 1: one plain product).
  * a: device codes [rows, k/2] + scales [rows, k/32]; w: device codes [groups, n, k/2] + scales
  * [groups, n, k/32]; out: device [rows, n] bf16.  offsets: device [groups + 1] int32, ascending in
- * [0, rows]; rows outside every group are not written.  A table that is not ascending or leaves
- * [0, rows] is clamped (no access is out of range), the outputs are undefined and
- * ft_moe_check(ws) returns FT_ERR_DEVICE_CHECK.
+ * [0, rows]; rows outside every group are not written.  For a table that is not ascending or
+ * leaves [0, rows] nothing is computed and ft_moe_check(ws) returns FT_ERR_DEVICE_CHECK.
  * groups <= 256, k % 64 == 0, k <= 16384, n % 8 == 0.  Codes and out 16-byte aligned, scales
  * 2-byte aligned (16-byte aligned scale rows load fastest).  ws: device workspace of
  * ft_mx4_product_workspace_bytes(...) bytes or more, prepared once by ft_moe_workspace_init;
@@ -362,8 +362,8 @@ ft_status ft_moe_permute_backward(const ft_moe_shape* shape, int32_t T, const vo
 /* Gradient of step 1 from the gradient of the gates (softmax over the kept logits; the other
  * logits' gradient is zero): dlogits[t,j] = g_j (d_g_j - sum_i g_i d_g_i), device output [T,k]
  * fp32, required.  dw_router: optional device output [E,H] fp32, sum over the pairs routed to e
- * of dlogits * x[t]; dbias: optional device output [E] fp32 (both overwritten; zero for an expert
- * without tokens, and for T = 0).  x: device [T,H] bf16 (needed for dw_router); topk_idx, offsets,
+ * of dlogits * x[t], fp32 sums; dbias: optional device output [E] fp32 (both overwritten; zero for
+ * an expert without tokens, and for T = 0).  x: device [T,H] bf16 (needed for dw_router); topk_idx, offsets,
  * sorted_flat (needed for dw_router or dbias); topk_w, d_topk_w: device [T,k] fp32.
  * ws: scratch of ft_moe_workspace_bytes(shape, T) bytes or more (its row regions are
  * overwritten). */

@@ -136,3 +136,38 @@ def test_reference_quantizer_is_nearest_even_on_every_border():
     assert np.signbit(got[17]) and np.signbit(got[20])
     code, scale = M.quantize(np.full((1, 32), 2.0 ** -140))
     assert scale[0, 0] == 0 and not (code & 7).any()
+
+
+class _Elsewhere:
+    """Stands for a tensor on another device than the current one."""
+    device = "cuda:1"
+
+    def __init__(self, d):
+        self.d = d
+
+    def data_ptr(self):
+        return FAKE
+
+    def get_device(self):
+        return self.d
+
+
+@pytest.mark.parametrize("where", [1, -1])
+def test_tensors_of_another_device_are_refused(monkeypatch, where):
+    import torch
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    here, there = _Elsewhere(0), _Elsewhere(where)
+    s = F.make_shape(256, 64, 8, 2)
+    mx = F.make_shape(256, 128, 8, 2, 0, F.FT_W_MXFP4)
+    w = F.make_weights(FAKE, FAKE, FAKE, FAKE)
+    calls = [
+        (F.ft_mx4_quantize, (4, 64, F.FT_T_BF16, here, 64, here, there, None)),
+        (F.ft_mx4_product, (2, 4, 64, 128, here, here, here, there, here, here, here, BIG)),
+        (F.ft_moe_experts_mx4, (mx, 4, w, here, here, there, here, here, BIG)),
+        (F.ft_moe_layer_forward_mx4, (mx, 4, here, there, None, w, here, None, None, here, BIG)),
+        (F.ft_moe_combine_backward, (s, 4, there, here, here, here, here, here)),
+        (F.ft_moe_permute_backward, (s, 4, here, here, None, None, None, there)),
+        (F.ft_moe_route_backward, (s, 4, here, here, here, there, here, here, here, here, here, here, BIG)),
+    ]
+    for fn, args in calls:
+        assert "current" in refused(F.FT_ERR_INVALID_ARG, fn, *args)
