@@ -328,3 +328,27 @@ def test_backward_captured_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, (d_o, d_w, dl, dw, db, dx)))
+
+
+@pytest.mark.parametrize("k", [8, 6, 5])
+def test_routing_arrays_off_their_alignment(k):
+    """inv_pos, gates, experts and logit gradients are plain int32 / fp32 arrays: any 4-byte aligned address."""
+    import torch
+    T, H, E, S = 50, 512, 16, 1
+    s = setup(T, H, E, k, S)
+    dy, o, dxs = normal(s, T, H), normal(s, s["R"], H), normal(s, s["R"], H)
+    wr = torch.randn(E, H, device="cuda")
+    dl = torch.randn(T, k, device="cuda")
+    d_o, d_w = combine_backward(s, dy, o)
+    dx = permute_backward(s, dxs, dl, wr)
+
+    def moved(t):
+        b = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+        b[1:] = t.reshape(-1)
+        return b[1:].view(t.shape)
+    for name in ("inv", "gates", "idx"):
+        s[name] = moved(s[name])
+    d_o2, d_w2 = combine_backward(s, dy, o)
+    dx2 = permute_backward(s, dxs, moved(dl), wr)
+    assert torch.equal(d_o.view(torch.int16), d_o2.view(torch.int16)) and torch.equal(d_w, d_w2)
+    assert torch.equal(dx.view(torch.int16), dx2.view(torch.int16))
