@@ -12,7 +12,8 @@ from expert_offload_serving_router_b200 import ftmoe as F
 pytestmark = pytest.mark.gpu
 
 CASES = [(1, 128, 1, 1, 0), (1, 2048, 128, 8, 1), (3, 256, 4, 2, 1), (7, 4096, 256, 6, 0), (33, 512, 8, 8, 0),
-         (100, 1152, 40, 5, 1), (513, 384, 5, 1, 0), (1500, 128, 16, 3, 1), (2049, 640, 128, 8, 0)]
+         (100, 1152, 40, 5, 1), (513, 384, 5, 1, 0), (1500, 128, 16, 3, 1), (2049, 640, 128, 8, 0),
+         (2100, 256, 7, 3, 1), (2301, 128, 256, 6, 1)]
 
 
 @pytest.fixture(scope="module", autouse=True)
