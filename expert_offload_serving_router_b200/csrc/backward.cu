@@ -21,10 +21,12 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 }
 
 // ------------------------------------------------------------------ combine
-// WPT warps per token (8 / WPT tokens per CTA): a lane takes 16-byte columns, loads dy and the k
-// rows' vectors together, writes the k scaled vectors and keeps k partial dot products, which a
-// transposing reduction (nine shuffles for eight sums) and, for WPT > 1, shared memory finish.
-template <int WPT>
+// WPT warps per token (8 / WPT tokens per CTA; 8: a CTA of blockDim warps per token): a lane takes 16-byte
+// columns, loads dy and the k rows' vectors together, writes the k scaled vectors and keeps k partial
+// dot products, which a transposing reduction (nine shuffles for eight sums) and, for WPT > 1, shared
+// memory finish.  KB bounds k: slots without a row cost their instructions all the same (4096 x 768,
+// k = 4: 20 us with eight slots, 11 with four; 4096 x 2048, k = 6: 45 with eight, 38 with six).
+template <int WPT, int KB>
 __global__ void __launch_bounds__(256) combine_backward_kernel(int T, int H, int k, int S, int R,
                                                                const uint16_t* __restrict__ dy,
                                                                const uint16_t* __restrict__ o,
@@ -33,16 +35,17 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(int T, int H, int
                                                                float* __restrict__ d_w) {
     __shared__ float part[8][8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int w = warp % WPT, tl = warp / WPT;
+    const int nw = WPT == 8 ? int(blockDim.x >> 5) : WPT;
+    const int w = WPT == 8 ? warp : warp % WPT, tl = WPT == 8 ? 0 : warp / WPT;
     const int64_t t = int64_t(blockIdx.x) * (8 / WPT) + tl;
     float dot[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) dot[j] = 0.f;
     if (t < T) {
-        int pos[kMaxTopK];
-        float g[kMaxTopK];
+        int pos[KB];
+        float g[KB];
 #pragma unroll
-        for (int j = 0; j < kMaxTopK; ++j) {
+        for (int j = 0; j < KB; ++j) {
             pos[j] = -1;
             g[j] = 0.f;
             if (j < k) {
@@ -57,19 +60,19 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(int T, int H, int
             ps = p >= 0 && p < R ? p : -1;
         }
         const int nv = H / 8;
-        for (int c = w * 32 + lane; c < nv; c += WPT * 32) {
+        for (int c = w * 32 + lane; c < nv; c += nw * 32) {
             const uint4 du = ldg_nc_v4(dy + t * H + c * 8);
-            uint4 ou[kMaxTopK];
+            uint4 ou[KB];
             if (d_w) {
 #pragma unroll
-                for (int j = 0; j < kMaxTopK; ++j)
+                for (int j = 0; j < KB; ++j)
                     ou[j] = pos[j] >= 0 ? ldg_nc_v4(o + int64_t(pos[j]) * H + c * 8) : make_uint4(0, 0, 0, 0);
             }
             float d[8];
             unpack8(du, d);
             if (d_w) {
 #pragma unroll
-                for (int j = 0; j < kMaxTopK; ++j) {
+                for (int j = 0; j < KB; ++j) {
                     float x[8];
                     unpack8(ou[j], x);
 #pragma unroll
@@ -78,7 +81,7 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(int T, int H, int
             }
             if (d_o) {
 #pragma unroll
-                for (int j = 0; j < kMaxTopK; ++j) {
+                for (int j = 0; j < KB; ++j) {
                     if (pos[j] < 0) continue;
                     float x[8];
 #pragma unroll
@@ -105,30 +108,47 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(int T, int H, int
     if (t < T && w == 0 && lane < k) {
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < WPT; ++i) s += part[tl * WPT + i][lane];
+        for (int i = 0; i < WPT; ++i)
+            if (i < nw) s += part[tl * WPT + i][lane];
         d_w[t * k + lane] = s;
     }
 }
 
+template <int WPT>
+static void combine_backward_go(int T, int H, int k, int S, int R, const uint16_t* dy, const uint16_t* o, const int32_t* inv_pos,
+                                const float* gw, uint16_t* d_o, float* d_w, cudaStream_t st) {
+    const unsigned grid = unsigned((int64_t(T) * WPT + 7) / 8);
+    // a CTA per token: the fewest warps that take a row in as many steps as eight would, so that few idle
+    // in the last one (4096 x 2816, k = 8: 65 us with six warps, 71 with eight)
+    const int pieces = (H + 255) / 256, steps = (pieces + 7) / 8;
+    const int threads = WPT == 8 ? 32 * ((pieces + steps - 1) / steps) : 256;
+    if (k <= 2) combine_backward_kernel<WPT, 2><<<grid, threads, 0, st>>>(T, H, k, S, R, dy, o, inv_pos, gw, d_o, d_w);
+    else if (k <= 4) combine_backward_kernel<WPT, 4><<<grid, threads, 0, st>>>(T, H, k, S, R, dy, o, inv_pos, gw, d_o, d_w);
+    else if (k <= 6) combine_backward_kernel<WPT, 6><<<grid, threads, 0, st>>>(T, H, k, S, R, dy, o, inv_pos, gw, d_o, d_w);
+    else combine_backward_kernel<WPT, kMaxTopK><<<grid, threads, 0, st>>>(T, H, k, S, R, dy, o, inv_pos, gw, d_o, d_w);
+}
+
 cudaError_t launch_combine_backward(int T, int H, int k, int S, int R, const uint16_t* dy, const uint16_t* o,
                                     const int32_t* inv_pos, const float* gw, uint16_t* d_o, float* d_w, cudaStream_t st) {
-    // as many warps as the row has 512-byte pieces (a lane then has a vector of its own), up to the CTA
-    if (H <= 256)
-        combine_backward_kernel<1><<<(T + 7) / 8, 256, 0, st>>>(T, H, k, S, R, dy, o, inv_pos, gw, d_o, d_w);
-    else if (H <= 512)
-        combine_backward_kernel<2><<<(T + 3) / 4, 256, 0, st>>>(T, H, k, S, R, dy, o, inv_pos, gw, d_o, d_w);
-    else if (H <= 1024)
-        combine_backward_kernel<4><<<(T + 1) / 2, 256, 0, st>>>(T, H, k, S, R, dy, o, inv_pos, gw, d_o, d_w);
-    else
-        combine_backward_kernel<8><<<T, 256, 0, st>>>(T, H, k, S, R, dy, o, inv_pos, gw, d_o, d_w);
+    // Few tokens: a CTA each (128 x 4096, k = 8: 4.8 us, 7.6 with four warps, 25.7 with one).  Long rows
+    // keep it when there are more than four of them per token (8192 x 4096, k = 8: 177 us, 195 with
+    // four warps), else take four (k = 4: 109, 114 with eight, 122 with one).  Short rows: a warp per token,
+    // as each has a lane reduction of its own to pay (8192 x 512, k = 8: 27 us, 49 with four, 55 with
+    // eight), but four while there are not enough tokens for that (512 x 1024: 4.5, 8.1 with one).
+    const int w = T <= 256 || (H > 1024 && k > 4) ? 8 : H > 1024 ? 4 : T <= 1024 && H > 256 ? 4 : 1;
+    if (w == 1) combine_backward_go<1>(T, H, k, S, R, dy, o, inv_pos, gw, d_o, d_w, st);
+    else if (w == 4) combine_backward_go<4>(T, H, k, S, R, dy, o, inv_pos, gw, d_o, d_w, st);
+    else combine_backward_go<8>(T, H, k, S, R, dy, o, inv_pos, gw, d_o, d_w, st);
     return cudaGetLastError();
 }
 
 // ------------------------------------------------------------------ permutation
 // One thread per 16-byte column of a token; the router's rows (fp32, two vectors per column) are
-// small enough to come from L2.
-template <bool ROUTER>
-__global__ void __launch_bounds__(256) permute_backward_kernel(int T, int nv, int k, int S, int E, int R,
+// small enough to come from L2.  KB bounds k, as above (4096 x 4096, k = 6: 56 us with eight slots, 44 with six;
+// 8192 x 4096, k = 1: 49 with four, 38 with two).  Registers are held at 40 and 64, for six and four CTAs
+// an SM (without a bound 8192 x 2048, k = 2 and a shared row: 27 us, with it 21; k = 8: 58.9 and 57.6).
+template <bool ROUTER, int KB>
+__global__ void __launch_bounds__(256, KB <= 4 ? 6 : 4) permute_backward_kernel(int T, int nv, int k, int S, int E, int R,
                                                                const uint16_t* __restrict__ dxs,
                                                                const int32_t* __restrict__ inv_pos,
                                                                const int32_t* __restrict__ idx,
@@ -138,11 +158,11 @@ __global__ void __launch_bounds__(256) permute_backward_kernel(int T, int nv, in
     if (at >= int64_t(T) * nv) return;
     const int t = int(at <= 0xFFFFFFFFll ? int64_t(uint32_t(at) / uint32_t(nv)) : at / nv);
     const int c = int(at - int64_t(t) * nv);
-    uint4 u[kMaxTopK + 1];
+    uint4 u[KB + 1];
 #pragma unroll
-    for (int j = 0; j < kMaxTopK + 1; ++j) {
+    for (int j = 0; j < KB + 1; ++j) {
         int p = -1;
-        if (j < kMaxTopK) { if (j < k) p = inv_pos[int64_t(t) * k + j]; }
+        if (j < KB) { if (j < k) p = inv_pos[int64_t(t) * k + j]; }
         else if (S) p = inv_pos[int64_t(T) * k + t];
         u[j] = p >= 0 && p < R ? ldg_nc_v4(dxs + (int64_t(p) * nv + c) * 8) : make_uint4(0, 0, 0, 0);
     }
@@ -151,18 +171,19 @@ __global__ void __launch_bounds__(256) permute_backward_kernel(int T, int nv, in
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
     if (ROUTER) {
         // four rows of W_r in flight (with a load, its sums, then the next: 38 us for 4096 x 2048, k = 8)
-        int e[kMaxTopK];
-        float d[kMaxTopK];
+        constexpr int kN = KB == 6 ? 3 : KB < 4 ? KB : 4;
+        int e[KB];
+        float d[KB];
 #pragma unroll
-        for (int j = 0; j < kMaxTopK; ++j) {
+        for (int j = 0; j < KB; ++j) {
             e[j] = j < k ? idx[int64_t(t) * k + j] : -1;
             d[j] = j < k ? dl[int64_t(t) * k + j] : 0.f;
         }
 #pragma unroll
-        for (int j0 = 0; j0 < kMaxTopK; j0 += 4) {
-            float4 w[4][2];
+        for (int j0 = 0; j0 < KB; j0 += kN) {
+            float4 w[kN][2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < kN; ++j) {
                 const int ej = e[j0 + j];
                 const float4* row = reinterpret_cast<const float4*>(wr) + (int64_t(ej) * nv + c) * 2;
                 const bool ok = ej >= 0 && ej < E;
@@ -170,7 +191,7 @@ __global__ void __launch_bounds__(256) permute_backward_kernel(int T, int nv, in
                 w[j][1] = ok ? __ldg(row + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < kN; ++j) {
                 const float dj = d[j0 + j];
                 const float4 a = w[j][0], b = w[j][1];
                 acc[0] = fmaf(dj, a.x, acc[0]); acc[1] = fmaf(dj, a.y, acc[1]); acc[2] = fmaf(dj, a.z, acc[2]); acc[3] = fmaf(dj, a.w, acc[3]);
@@ -179,7 +200,7 @@ __global__ void __launch_bounds__(256) permute_backward_kernel(int T, int nv, in
         }
     }
 #pragma unroll
-    for (int j = 0; j < kMaxTopK + 1; ++j) {
+    for (int j = 0; j < KB + 1; ++j) {
         float f[8];
         unpack8(u[j], f);
 #pragma unroll
@@ -192,11 +213,12 @@ __global__ void __launch_bounds__(256) permute_backward_kernel(int T, int nv, in
 // twice the bytes of dx_sorted itself, so a CTA keeps W_r's 64-column slice (E x 256 bytes) in
 // shared memory and takes a run of tokens through it, eight lanes a token, eight columns a lane.  The
 // next tokens' positions, experts and gradients load while the current rows are summed.  Sums in the
-// order of the kernel above: the same bits.  8191 tokens x 2816, k = 8, a shared row: 87 -> 76 us (504 MB,
+// order of the kernel above: the same bits.  8191 tokens x 2816, k = 8, a shared row: 84 -> 76 us (504 MB,
 // 6.1 TB/s); 512 threads a CTA, one CTA an SM, had left it at 96.
 constexpr int kPbThreads = 256;
 constexpr int kPbTokens = kPbThreads / 8;     // tokens a pass
 
+template <int KB>
 __global__ void __launch_bounds__(kPbThreads, 3) permute_backward_slice_kernel(int T, int H, int k, int S, int E, int R,
                                                                             int run, const uint16_t* __restrict__ dxs,
                                                                             const int32_t* __restrict__ inv_pos,
@@ -235,13 +257,13 @@ __global__ void __launch_bounds__(kPbThreads, 3) permute_backward_slice_kernel(i
     const int first = tid & 24;                     // the token's first lane in the warp
     for (int64_t base = t0; base < end; base += kPbTokens) {
         const int64_t t = base + (tid >> 3);
-        uint4 u[kMaxTopK + 1];
+        uint4 u[KB + 1];
 #pragma unroll
-        for (int j = 0; j < kMaxTopK; ++j) {
+        for (int j = 0; j < KB; ++j) {
             const int p = __shfl_sync(0xffffffffu, pos, first + j);
             u[j] = p >= 0 && p < R ? ldg_nc_v4(dxs + int64_t(p) * H + col) : make_uint4(0, 0, 0, 0);
         }
-        u[kMaxTopK] = ps >= 0 && ps < R ? ldg_nc_v4(dxs + int64_t(ps) * H + col) : make_uint4(0, 0, 0, 0);
+        u[KB] = ps >= 0 && ps < R ? ldg_nc_v4(dxs + int64_t(ps) * H + col) : make_uint4(0, 0, 0, 0);
         const int e_now = e;
         const float d_now = d;
         fetch(base + kPbTokens);
@@ -249,7 +271,7 @@ __global__ void __launch_bounds__(kPbThreads, 3) permute_backward_slice_kernel(i
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i] = 0.f;
 #pragma unroll
-        for (int j = 0; j < kMaxTopK; ++j) {
+        for (int j = 0; j < KB; ++j) {
             const int ej = __shfl_sync(0xffffffffu, e_now, first + j);
             const float dj = __shfl_sync(0xffffffffu, d_now, first + j);
             const bool ok = ej >= 0 && ej < E;
@@ -260,7 +282,7 @@ __global__ void __launch_bounds__(kPbThreads, 3) permute_backward_slice_kernel(i
             acc[4] = fmaf(dj, b.x, acc[4]); acc[5] = fmaf(dj, b.y, acc[5]); acc[6] = fmaf(dj, b.z, acc[6]); acc[7] = fmaf(dj, b.w, acc[7]);
         }
 #pragma unroll
-        for (int j = 0; j < kMaxTopK + 1; ++j) {
+        for (int j = 0; j < KB + 1; ++j) {
             float f[8];
             unpack8(u[j], f);
 #pragma unroll
@@ -270,10 +292,15 @@ __global__ void __launch_bounds__(kPbThreads, 3) permute_backward_slice_kernel(i
     }
 }
 
-cudaError_t launch_permute_backward(int T, int H, int k, int S, int E, int R, const uint16_t* dxs, const int32_t* inv_pos,
-                                    const int32_t* idx, const float* dl, const float* wr, uint16_t* dx, cudaStream_t st) {
+template <int KB>
+static cudaError_t permute_backward_go(int T, int H, int k, int S, int E, int R, const uint16_t* dxs, const int32_t* inv_pos,
+                                       const int32_t* idx, const float* dl, const float* wr, uint16_t* dx, cudaStream_t st) {
     const int nv = H / 8;
-    if (wr && T >= 2048) {
+    // Pays once dx_sorted is far larger than L2, so that W_r's rows no longer stay there: E = 128, 4096 columns,
+    // 8192 tokens: k = 5 (336 MB) 89 us without, 79 with; k = 8 (537 MB) 124 and 113; but 8192 x 2048, k = 8 and
+    // a shared row (302 MB), 59.2 and 60.2, with E = 256 61 and 66.  Few rows a token: 70 and 64 (k = 4, 268 MB)
+    // before the register bound above, 65 since.
+    if (wr && KB > 4 && (int64_t(k) + S) * T * H * 2 >= (320ll << 20)) {
         // two waves of three CTAs an SM, not a CTA more (each reads its slice of W_r once)
         const int slices = H / 64;
         int64_t runs = 6 * num_sms() / slices > 0 ? 6 * num_sms() / slices : 1;
@@ -283,18 +310,27 @@ cudaError_t launch_permute_backward(int T, int H, int k, int S, int E, int R, co
         const size_t smem = size_t(E) * 256;
         static PerDeviceOnce attr;
         const cudaError_t e = attr([&] {
-            return cudaFuncSetAttribute(permute_backward_slice_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxExperts * 256);
+            return cudaFuncSetAttribute(permute_backward_slice_kernel<KB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        kMaxExperts * 256);
         });
         if (e != cudaSuccess) return e;
-        permute_backward_slice_kernel<<<dim3(slices, unsigned(runs)), kPbThreads, smem, st>>>(T, H, k, S, E, R, int(run), dxs,
-                                                                                              inv_pos, idx, dl, wr, dx);
+        permute_backward_slice_kernel<KB><<<dim3(slices, unsigned(runs)), kPbThreads, smem, st>>>(
+            T, H, k, S, E, R, int(run), dxs, inv_pos, idx, dl, wr, dx);
         return cudaGetLastError();
     }
     const int64_t blocks = (int64_t(T) * nv + 255) / 256;
     if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-    if (wr) permute_backward_kernel<true><<<unsigned(blocks), 256, 0, st>>>(T, nv, k, S, E, R, dxs, inv_pos, idx, dl, wr, dx);
-    else permute_backward_kernel<false><<<unsigned(blocks), 256, 0, st>>>(T, nv, k, S, E, R, dxs, inv_pos, idx, dl, wr, dx);
+    if (wr) permute_backward_kernel<true, KB><<<unsigned(blocks), 256, 0, st>>>(T, nv, k, S, E, R, dxs, inv_pos, idx, dl, wr, dx);
+    else permute_backward_kernel<false, KB><<<unsigned(blocks), 256, 0, st>>>(T, nv, k, S, E, R, dxs, inv_pos, idx, dl, wr, dx);
     return cudaGetLastError();
+}
+
+cudaError_t launch_permute_backward(int T, int H, int k, int S, int E, int R, const uint16_t* dxs, const int32_t* inv_pos,
+                                    const int32_t* idx, const float* dl, const float* wr, uint16_t* dx, cudaStream_t st) {
+    if (k <= 2) return permute_backward_go<2>(T, H, k, S, E, R, dxs, inv_pos, idx, dl, wr, dx, st);
+    if (k <= 4) return permute_backward_go<4>(T, H, k, S, E, R, dxs, inv_pos, idx, dl, wr, dx, st);
+    if (k <= 6) return permute_backward_go<6>(T, H, k, S, E, R, dxs, inv_pos, idx, dl, wr, dx, st);
+    return permute_backward_go<kMaxTopK>(T, H, k, S, E, R, dxs, inv_pos, idx, dl, wr, dx, st);
 }
 
 // ------------------------------------------------------------------ router
@@ -326,6 +362,9 @@ __device__ __forceinline__ int routed_rows(const RouteBackward& a) { return max(
 // Small batches (P <= kRbSmall), one launch: CTA (expert, 256 columns), the expert's rows dealt to
 // eight warps, their sums joined through shared memory in warp order.  CTA e also writes the e-th
 // share of dlogits.
+// One launch against three, us: 6 x 128 rows at 4096 columns, E = 256: 9.9 and 13.2; 8 x 128 at 2048: 5.9 and
+// 9.8; 8 x 256: 8.5 and 10.4; 8 x 512: 14.0 and 11.9.  The bound is below the crossing, as an expert's rows are one
+// CTA's work here: 1024 rows in four experts 9.9 and 8.1.
 constexpr int kRbSmall = 1024;
 
 __global__ void __launch_bounds__(256) route_backward_small_kernel(RouteBackward a) {
@@ -508,8 +547,10 @@ __global__ void __launch_bounds__(256) route_backward_join_kernel(RouteBackward 
     if (a.db && blockIdx.y == 0 && lane == 0) a.db[e] = sb;
 }
 
-// rows per segment: short ones until they fill the SMs, then longer ones (fewer partial sums)
-static int route_segment(int P) { return P <= 16384 ? 16 : kRbMaxSeg; }
+// rows per segment: short ones until they fill the SMs, then longer ones (fewer partial sums).  16 against
+// 64 rows, us: 6 x 680 at 4096 columns 17.2 and 20.0; 8 x 1024 at 2048 14.6 and 16.4; 6 x 2000 at 4096 28.7
+// and 25.9; 8 x 2048 at 2048 20.9 and 19.0; 6 x 5460 at 4096 55.9 and 44.9
+static int route_segment(int P) { return P <= 8192 ? 16 : kRbMaxSeg; }
 
 // scratch at `part`, as laid out below; nothing for small batches
 size_t route_backward_part_bytes(int T, int H, int k) {

@@ -541,12 +541,6 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                 const PxTile tl = tile_at(lt, lj);
                 src[0] = weight_row(tl);
                 take[0] = true;
-                // the next tile's weight scales into L2: behind the code stream a load from DRAM takes
-                // longer than a chunk's MMAs
-                if (grp == 0 && lt + stride < total) {
-                    const uint8_t* nx = weight_row(tile_at(lt + stride, lj + 1));
-                    for (int o = 0; o < nsc; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(nx + o));
-                }
 #pragma unroll
                 for (int h = 0; h < C::kHalves; ++h) {
                     take[1 + h] = i + 128 * h < ((tl.nvalid + 15) & ~15);

@@ -110,6 +110,56 @@ def test_permute_backward(T, H, E, k, S, router):
     assert ((dx.double() - want).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("T,H,E,k,S", [(4600, 4096, 256, 8, 1), (6900, 4096, 7, 5, 1), (16500, 1280, 33, 8, 0), (27400, 1024, 64, 6, 0),
+                                       (164001, 128, 8, 8, 0)])
+def test_permute_backward_rows_beyond_the_cache(T, H, E, k, S):
+    """dx_sorted above 320 MB: the form with W_r's slice in shared memory; a few tokens of it alone (the other form) give
+    the same bits."""
+    import torch
+    s = setup(T, H, E, k, S)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    dxs = torch.randn(s["R"], H, device="cuda", generator=gen).to(torch.bfloat16)
+    dl, wr = torch.randn(T, k, device="cuda", generator=gen), torch.randn(E, H, device="cuda", generator=gen)
+    dx = permute_backward(s, dxs, dl, wr)
+    pos = s["inv"].long()
+    for lo in range(0, T, 20000):
+        hi = min(T, lo + 20000)
+        terms = dxs.double()[pos[lo * k:hi * k]].view(hi - lo, k, H)
+        if S:
+            terms = torch.cat([terms, dxs.double()[pos[T * k + lo:T * k + hi]][:, None]], 1)
+        terms = torch.cat([terms, dl[lo:hi].double()[..., None] * wr.double()[s["idx"][lo:hi].long()]], 1)
+        want, mag = terms.sum(1), terms.abs().sum(1)
+        tol = M.UB16 * want.abs() + (terms.shape[1] + 1) * M.U32 * (1 + M.UB16) * mag
+        assert ((dx[lo:hi].double() - want).abs() <= tol).all()
+    n, at = 50, T - 57
+    few = dict(s, T=n, shape=F.make_shape(H, 64, E, k, S))
+    few["idx"] = s["idx"][at:at + n].contiguous()
+    few["inv"] = torch.arange(n * (k + S), dtype=torch.int32, device="cuda")
+    rows = torch.cat([pos[at * k:(at + n) * k]] + ([pos[T * k + at:T * k + at + n]] if S else []))
+    alone = permute_backward(few, dxs[rows].contiguous(), dl[at:at + n].contiguous(), wr)
+    assert torch.equal(alone.view(torch.int16), dx[at:at + n].view(torch.int16))
+
+
+@pytest.mark.parametrize("H", [128, 384, 1024, 1280, 2816])
+@pytest.mark.parametrize("T", [256, 257, 1025])
+@pytest.mark.parametrize("k,S", [(1, 0), (2, 1), (3, 0), (5, 1), (6, 0), (7, 1)])
+def test_combine_backward_warps_per_token(T, H, k, S):
+    """Both sides of the bounds on tokens, columns and k that choose how many warps take a token and how many slots they hold."""
+    import torch
+    s = setup(T, H, 9, k, S)
+    dy, o = normal(s, T, H, std=0.1), normal(s, s["R"], H)
+    d_o, d_w = combine_backward(s, dy, o)
+    pos = s["inv"].long()
+    routed = pos[:T * k].view(T, k)
+    want = torch.empty_like(d_o)
+    want[routed] = (s["gates"][..., None] * dy.float()[:, None]).to(torch.bfloat16)
+    if S:
+        want[pos[T * k:]] = dy
+    assert torch.equal(d_o.view(torch.int16), want.view(torch.int16))
+    terms = o.double()[routed] * dy.double()[:, None]
+    assert ((d_w.double() - terms.sum(-1)).abs() <= H * M.U32 * terms.abs().sum(-1)).all()
+
+
 def route_backward(s, x, dg, want_w=True, want_b=True):
     import torch
     E, H, T, k = s["E"], s["H"], s["T"], s["k"]
