@@ -154,6 +154,11 @@ __device__ __forceinline__ bool px_wait_all_pair(uint64_t* b, uint32_t parity, v
     if constexpr (PAIR) return __all_sync(0xffffffffu, mbar_wait_cluster(b, parity, abort, limit)) != 0;
     else return px_wait_all(b, parity, abort, limit);
 }
+template <bool PAIR>
+__device__ __forceinline__ bool px_wait_pair(uint64_t* b, uint32_t parity, volatile int* abort, unsigned long long limit) {
+    if constexpr (PAIR) return mbar_wait_cluster(b, parity, abort, limit);
+    else return px_wait(b, parity, abort, limit);
+}
 __device__ __forceinline__ bool px_elect() {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
@@ -448,25 +453,27 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
             const uint32_t dacc = tmem + uint32_t(BN * buf);
             const uint32_t id0 = idesc_mxf4(PAIR ? 256 : 128, N, 0), id2 = idesc_mxf4(PAIR ? 256 : 128, N, 2);
             const bool two = C::kHalves == 2 && N > 128;
-            for (int kb = 0; kb < nk; ++kb) {
-                if ((kb & (kPxChunk - 1)) == 0) {
-                    ok = px_wait_all_pair<PAIR>(&sfull[ch % kPxSfBufs], uint32_t(ch / kPxSfBufs) & 1u, abort_flag, p.wait_ns);
+            if (leader) {
+                int st = s, c = ch;
+                uint32_t ph = phase;
+                for (int kb = 0; kb < nk; ++kb) {
+                    if ((kb & (kPxChunk - 1)) == 0) {
+                        ok = px_wait_pair<PAIR>(&sfull[c % kPxSfBufs], uint32_t(c / kPxSfBufs) & 1u, abort_flag, p.wait_ns);
+                        if (!ok) break;
+                    }
+                    ok = px_wait(&full[st], ph, abort_flag, p.wait_ns);
                     if (!ok) break;
-                }
-                ok = px_wait_all(&full[s], phase, abort_flag, p.wait_ns);
-                if (!ok) break;
-                tc_fence_after();
-                const bool chunk_end = (kb & (kPxChunk - 1)) == kPxChunk - 1 || kb == nk - 1;
-                if (leader) {
-                    const uint32_t sfa = tmem + uint32_t(C::kSfBase + (s & 1) * C::kSfCols), sfb = sfa + 8u;
-                    const uint64_t sd = sf0 + uint64_t(((ch % kPxSfBufs) * C::kSfChunk + (kb & (kPxChunk - 1)) * C::kSfBytes) >> 4);
+                    tc_fence_after();
+                    const bool chunk_end = (kb & (kPxChunk - 1)) == kPxChunk - 1 || kb == nk - 1;
+                    const uint32_t sfa = tmem + uint32_t(C::kSfBase + (st & 1) * C::kSfCols), sfb = sfa + 8u;
+                    const uint64_t sd = sf0 + uint64_t(((c % kPxSfBufs) * C::kSfChunk + (kb & (kPxChunk - 1)) * C::kSfBytes) >> 4);
 #pragma unroll
                     for (int a = 0; a < 2; ++a) {
                         px_copy_atom<PAIR>(sfa + 4u * a, sd + uint64_t(32 * a));
                         px_copy_atom<PAIR>(sfb + 4u * C::kHalves * a, sd + uint64_t((C::kSfA + a * C::kHalves * 512) >> 4));
                         if (two) px_copy_atom<PAIR>(sfb + 4u * C::kHalves * a + 4u, sd + uint64_t((C::kSfA + a * C::kHalves * 512 + 512) >> 4));
                     }
-                    const uint64_t ad = ad0 + uint64_t((s * kPxABytes) >> 4), bd = bd0 + uint64_t((s * C::kBBytes) >> 4);
+                    const uint64_t ad = ad0 + uint64_t((st * kPxABytes) >> 4), bd = bd0 + uint64_t((st * C::kBBytes) >> 4);
                     const int steps = min(4, (p.K - kb * kPxK) >> 6);       // 64-deep MMAs of this stage
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -475,16 +482,17 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                         umma_mxf4<PAIR>(dacc, ad + uint64_t(2 * i), bd + uint64_t(2 * i), (i & 1) ? id2 : id0,
                                   (sfa + 4u * (i >> 1)) | hi, (sfb + 4u * C::kHalves * (i >> 1)) | hi, (kb | i) != 0);
                     }
-                    px_commit<PAIR>(&empty[s]);
-                    if (chunk_end) px_commit<PAIR>(&sempty[ch % kPxSfBufs]);
+                    px_commit<PAIR>(&empty[st]);
+                    if (chunk_end) { px_commit<PAIR>(&sempty[c % kPxSfBufs]); ++c; }
+                    if (++st == kSt) { st = 0; ph ^= 1u; }
                 }
-                __syncwarp();
-                if (chunk_end) ++ch;
-                if (++s == kSt) { s = 0; phase ^= 1u; }
+                if (ok) px_commit<PAIR>(&tfull[buf]);
             }
+            ok = __all_sync(0xffffffffu, ok) != 0;
             if (!ok) break;
-            if (leader) px_commit<PAIR>(&tfull[buf]);
-            __syncwarp();
+            ch += (nk + kPxChunk - 1) / kPxChunk;
+            phase ^= uint32_t((s + nk) / kSt) & 1u;
+            s = (s + nk) % kSt;
         }
         if (PAIR && rank == 1 && lane == 0) {
             // The peer's idle issuer passes its epilogue's arrivals on to the leader: one cluster-scope release
