@@ -456,6 +456,8 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
             if (leader) {
                 int st = s, c = ch;
                 uint32_t ph = phase;
+                const int full_k = p.K / kPxK;
+#pragma unroll 4
                 for (int kb = 0; kb < nk; ++kb) {
                     if ((kb & (kPxChunk - 1)) == 0) {
                         ok = px_wait_pair<PAIR>(&sfull[c % kPxSfBufs], uint32_t(c / kPxSfBufs) & 1u, abort_flag, p.wait_ns);
@@ -465,7 +467,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                     if (!ok) break;
                     tc_fence_after();
                     const bool chunk_end = (kb & (kPxChunk - 1)) == kPxChunk - 1 || kb == nk - 1;
-                    const uint32_t sfa = tmem + uint32_t(C::kSfBase + (st & 1) * C::kSfCols), sfb = sfa + 8u;
+                    const uint32_t sfa = tmem + uint32_t(C::kSfBase + (kb & 1) * C::kSfCols), sfb = sfa + 8u;
                     const uint64_t sd = sf0 + uint64_t(((c % kPxSfBufs) * C::kSfChunk + (kb & (kPxChunk - 1)) * C::kSfBytes) >> 4);
 #pragma unroll
                     for (int a = 0; a < 2; ++a) {
@@ -474,13 +476,17 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                         if (two) px_copy_atom<PAIR>(sfb + 4u * C::kHalves * a + 4u, sd + uint64_t((C::kSfA + a * C::kHalves * 512 + 512) >> 4));
                     }
                     const uint64_t ad = ad0 + uint64_t((st * kPxABytes) >> 4), bd = bd0 + uint64_t((st * C::kBBytes) >> 4);
-                    const int steps = min(4, (p.K - kb * kPxK) >> 6);       // 64-deep MMAs of this stage
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (i >= steps) break;
+                    const auto mma = [&](int i) {            // 64 deep
                         const uint32_t hi = (i & 1) ? 2u << 30 : 0u;
                         umma_mxf4<PAIR>(dacc, ad + uint64_t(2 * i), bd + uint64_t(2 * i), (i & 1) ? id2 : id0,
                                   (sfa + 4u * (i >> 1)) | hi, (sfb + 4u * C::kHalves * (i >> 1)) | hi, (kb | i) != 0);
+                    };
+                    if (kb < full_k) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mma(i);
+                    } else {
+#pragma unroll 1
+                        for (int i = 0; i < ((p.K >> 6) & 3); ++i) mma(i);
                     }
                     px_commit<PAIR>(&empty[st]);
                     if (chunk_end) { px_commit<PAIR>(&sempty[c % kPxSfBufs]); ++c; }
