@@ -148,12 +148,35 @@ __device__ __forceinline__ bool px_warp_wait(uint64_t* b, uint32_t parity, volat
 __device__ __forceinline__ bool px_wait_all(uint64_t* b, uint32_t parity, volatile int* abort, unsigned long long limit) {
     return __all_sync(0xffffffffu, px_wait(b, parity, abort, limit)) != 0;
 }
-// the same on a barrier that the pair's other CTA arrives on too
+// An accumulator handed back across the pair: tensor memory alone, which the tcgen05 fences before the
+// arrival and after the wait order.  Both are relaxed: a release at cluster scope would wait for the
+// epilogue's stores (2000 to 3500 clocks a tile), which nobody reads here.
+__device__ __forceinline__ void px_release_tmem(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ bool px_try_tmem(uint64_t* b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(su32(b)), "r"(parity) : "memory");
+    return ok != 0;
+}
+static __device__ __noinline__ bool px_wait_tmem_slow(uint64_t* b, uint32_t parity, volatile int* abort, unsigned long long limit) {
+    const uint64_t t0 = gtimer();
+    for (uint32_t i = 1;; ++i) {
+        if (px_try_tmem(b, parity)) return true;
+        if ((i & 31) == 0 || limit < kWaitNs) {
+            if (abort && *abort) return false;
+            if (gtimer() - t0 > limit) return false;
+        }
+    }
+}
 template <bool PAIR>
-__device__ __forceinline__ bool px_wait_all_pair(uint64_t* b, uint32_t parity, volatile int* abort, unsigned long long limit) {
-    if constexpr (PAIR) return __all_sync(0xffffffffu, mbar_wait_cluster(b, parity, abort, limit)) != 0;
+__device__ __forceinline__ bool px_wait_all_tmem(uint64_t* b, uint32_t parity, volatile int* abort, unsigned long long limit) {
+    if constexpr (PAIR) return __all_sync(0xffffffffu, px_try_tmem(b, parity) || px_wait_tmem_slow(b, parity, abort, limit)) != 0;
     else return px_wait_all(b, parity, abort, limit);
 }
+// a barrier that the pair's other CTA arrives on too
 template <bool PAIR>
 __device__ __forceinline__ bool px_wait_pair(uint64_t* b, uint32_t parity, volatile int* abort, unsigned long long limit) {
     if constexpr (PAIR) return mbar_wait_cluster(b, parity, abort, limit);
@@ -302,7 +325,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], kPxEpi + (PAIR && rank == 0));            // own warps, and for the leader the peer's forwarder
+            mbar_init(&tempty[b], PAIR ? 2 * kPxEpi : kPxEpi);      // a pair's epilogue warps all arrive at the leader
         }
         for (int b = 0; b < kPxSfBufs; ++b) {
             mbar_init(&sfull[b], PAIR ? kPxLoaders : kPxLoaders / 2);      // one group's warps, in a pair of both CTAs
@@ -447,7 +470,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
             const PxTile tl = tile_at(t, j);
             const int N = __shfl_sync(0xffffffffu, (tl.nvalid + 15) & ~15, 0);
             const int buf = j & 1;
-            ok = px_wait_all_pair<PAIR>(&tempty[buf], (uint32_t(j >> 1) & 1u) ^ 1u, abort_flag, p.wait_ns);
+            ok = px_wait_all_tmem<PAIR>(&tempty[buf], (uint32_t(j >> 1) & 1u) ^ 1u, abort_flag, p.wait_ns);
             if (!ok) break;
             tc_fence_after();
             const uint32_t dacc = tmem + uint32_t(BN * buf);
@@ -499,16 +522,6 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
             ch += (nk + kPxChunk - 1) / kPxChunk;
             phase ^= uint32_t((s + nk) / kSt) & 1u;
             s = (s + nk) % kSt;
-        }
-        if (PAIR && rank == 1 && lane == 0) {
-            // The peer's idle issuer passes its epilogue's arrivals on to the leader: one cluster-scope release
-            // per tile (some 2000 clocks under load, behind the epilogue's stores) instead of eight.
-            int j = 0;
-            for (int t = first; t < total; t += stride, ++j) {
-                if (!px_wait(&tempty[j & 1], uint32_t(j >> 1) & 1u, abort_flag, p.wait_ns)) { ok = false; break; }
-                mbar_arrive_cluster(tempty_lead + 8u * (j & 1));
-            }
-            if (!ok) { *abort_flag = 1; atomicExch(p.err, kDevErrTimeout); }
         }
         __syncwarp();
         if (leader) {
@@ -598,6 +611,11 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
         const int half = (warp - 2 - kPxLoaders) >> 2;   // column chunks half, half + 2, ...
         // SwiGLU: the two warps of a lane half of the accumulator share the 32 columns of h of one MXFP4 block
         const int duo = 2 * half + (q >> 1), et = 32 * (q & 1) + lane;      // pair 0..3, thread 0..63 of it
+        const auto release = [&](int buf) {
+            if (lane) return;
+            if constexpr (PAIR) px_release_tmem(tempty_lead + 8u * buf);
+            else mbar_arrive(&tempty[buf]);
+        };
         bool ok = true;
         int j = 0;
         for (int t = first; t < total; t += stride, ++j) {
@@ -632,7 +650,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                 if (c + 2 >= nch) {                    // this warp's last read of the accumulator
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&tempty[buf]);
+                    release(buf);
                 }
                 if constexpr (SWIGLU) {
                     // the first 16 rows are gate rows f, the second the up rows of the same f: both in the same
@@ -698,7 +716,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
             if (half >= nch) {                         // no chunk of this tile is this warp's
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&tempty[buf]);
+                release(buf);
             }
         }
         if (!ok) { *abort_flag = 1; if (lane == 0) atomicExch(p.err, kDevErrTimeout); }
