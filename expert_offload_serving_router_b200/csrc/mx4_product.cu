@@ -237,30 +237,35 @@ __device__ __forceinline__ PxTile px_tile(int t, const int* ntile, const int* of
 
 // 32 scale bytes (1024 elements) of a row, from byte 32 c on.  Bytes past the row's nsc are whatever
 // is there: the MMAs stop at K.  Rows that start off an 8-byte boundary (K / 32 not a multiple of 8)
-// are read as the aligned 8-byte words that hold them and shifted into place -- a word is read
-// only if it holds a byte of the row, so no read leaves the allocation.
-__device__ __forceinline__ void px_load_scales(const uint8_t* row, int c, int nsc, int vec, uint32_t (&v)[8]) {
+// are read as the aligned 8-byte words that hold them -- a word is read only if it holds a byte of the
+// row, so no read leaves the allocation -- and shifted into place when they are laid out: shifting them
+// here would wait for the loads.
+__device__ __forceinline__ void px_load_scales(const uint8_t* row, int c, int nsc, int vec, uint64_t (&u)[5]) {
     const int o = 32 * c, n = min(32, nsc - o);
     if (vec == 16) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             if (16 * i < n) {
-                const uint4 u = *reinterpret_cast<const uint4*>(row + o + 16 * i);
-                v[4 * i] = u.x; v[4 * i + 1] = u.y; v[4 * i + 2] = u.z; v[4 * i + 3] = u.w;
+                const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(row + o + 16 * i);
+                u[2 * i] = w.x;
+                u[2 * i + 1] = w.y;
             }
     } else {
         const uintptr_t at = reinterpret_cast<uintptr_t>(row + o);
         const uint64_t* w = reinterpret_cast<const uint64_t*>(at & ~uintptr_t(7));
-        const int lead = int(at & 7), sh = 8 * lead;
-        uint64_t u[5];
+        const int lead = int(at & 7);
 #pragma unroll
         for (int i = 0; i < 5; ++i) u[i] = 8 * i < lead + n ? w[i] : 0;
+    }
+}
+// the eight 4-byte pieces of the row at `row`
+__device__ __forceinline__ void px_scale_words(const uint8_t* row, const uint64_t (&u)[5], uint32_t (&v)[8]) {
+    const int sh = 8 * int(reinterpret_cast<uintptr_t>(row) & 7);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint64_t x = sh ? (u[i] >> sh) | (u[i + 1] << (64 - sh)) : u[i];
-            v[2 * i] = uint32_t(x);
-            v[2 * i + 1] = uint32_t(x >> 32);
-        }
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t x = sh ? (u[i] >> sh) | (u[i + 1] << (64 - sh)) : u[i];
+        v[2 * i] = uint32_t(x);
+        v[2 * i + 1] = uint32_t(x >> 32);
     }
 }
 
@@ -542,7 +547,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
         const int nsc = p.K / 32, nch = (nk + kPxChunk - 1) / kPxChunk;
         const int at = 16 * (i & 31) + 4 * (i >> 5);
         constexpr int kRows = 1 + C::kHalves;
-        uint32_t v[kRows][8] = {};
+        uint64_t raw[kRows][5] = {};
         int lt = first, lj = 0, lc = 0, cur = -1;      // the load cursor, and the tile its row pointers are of
         const uint8_t* src[kRows] = {};
         bool take[kRows] = {};
@@ -576,7 +581,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
             }
 #pragma unroll
             for (int r = 0; r < kRows; ++r)
-                if (take[r]) px_load_scales(src[r], lc, nsc, p.vec, v[r]);
+                if (take[r]) px_load_scales(src[r], lc, nsc, p.vec, raw[r]);
         };
         bool ok = true;
         pdl_wait();                            // the activations' scales come from the preceding kernel
@@ -586,6 +591,9 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
             const int b = ch % kPxSfBufs;
             if (!px_warp_wait(&sempty[b], (uint32_t(ch / kPxSfBufs) & 1u) ^ 1u, abort_flag, p.wait_ns)) { ok = false; break; }
             uint8_t* d = sSf + b * C::kSfChunk + at;
+            uint32_t v[kRows][8];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) px_scale_words(src[r], raw[r], v[r]);     // src: still this chunk's tile
 #pragma unroll
             for (int sub = 0; sub < kPxChunk; ++sub)
 #pragma unroll
