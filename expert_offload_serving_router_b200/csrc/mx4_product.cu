@@ -148,38 +148,40 @@ __device__ __forceinline__ bool px_warp_wait(uint64_t* b, uint32_t parity, volat
 __device__ __forceinline__ bool px_wait_all(uint64_t* b, uint32_t parity, volatile int* abort, unsigned long long limit) {
     return __all_sync(0xffffffffu, px_wait(b, parity, abort, limit)) != 0;
 }
-// An accumulator handed back across the pair: tensor memory alone, which the tcgen05 fences before the
-// arrival and after the wait order.  Both are relaxed: a release at cluster scope would wait for the
-// epilogue's stores (2000 to 3500 clocks a tile), which nobody reads here.
-__device__ __forceinline__ void px_release_tmem(uint32_t cluster_addr) {
+// Signals across the pair are relaxed, and what they hand over is ordered beside them: a release at cluster
+// scope waits for the epilogue's global stores (2000 to 3600 clocks each time), which nobody reads here.
+//   accumulators: tensor memory alone, ordered by the tcgen05 fences before the arrival and after the wait
+//   scale chunks: shared memory alone, ordered by fences restricted to it (px_release_shared / px_acquire_shared)
+__device__ __forceinline__ void px_arrive_peer(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-__device__ __forceinline__ bool px_try_tmem(uint64_t* b, uint32_t parity) {
+__device__ __forceinline__ void px_release_shared() {
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+}
+__device__ __forceinline__ void px_acquire_shared() {
+    asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+}
+__device__ __forceinline__ bool px_try_peer(uint64_t* b, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok) : "r"(su32(b)), "r"(parity) : "memory");
     return ok != 0;
 }
-static __device__ __noinline__ bool px_wait_tmem_slow(uint64_t* b, uint32_t parity, volatile int* abort, unsigned long long limit) {
+static __device__ __noinline__ bool px_wait_peer_slow(uint64_t* b, uint32_t parity, volatile int* abort, unsigned long long limit) {
     const uint64_t t0 = gtimer();
     for (uint32_t i = 1;; ++i) {
-        if (px_try_tmem(b, parity)) return true;
+        if (px_try_peer(b, parity)) return true;
         if ((i & 31) == 0 || limit < kWaitNs) {
             if (abort && *abort) return false;
             if (gtimer() - t0 > limit) return false;
         }
     }
 }
+// barriers that the pair's other CTA arrives on too
 template <bool PAIR>
-__device__ __forceinline__ bool px_wait_all_tmem(uint64_t* b, uint32_t parity, volatile int* abort, unsigned long long limit) {
-    if constexpr (PAIR) return __all_sync(0xffffffffu, px_try_tmem(b, parity) || px_wait_tmem_slow(b, parity, abort, limit)) != 0;
-    else return px_wait_all(b, parity, abort, limit);
-}
-// a barrier that the pair's other CTA arrives on too
-template <bool PAIR>
-__device__ __forceinline__ bool px_wait_pair(uint64_t* b, uint32_t parity, volatile int* abort, unsigned long long limit) {
-    if constexpr (PAIR) return mbar_wait_cluster(b, parity, abort, limit);
+__device__ __forceinline__ bool px_wait_peer(uint64_t* b, uint32_t parity, volatile int* abort, unsigned long long limit) {
+    if constexpr (PAIR) return px_try_peer(b, parity) || px_wait_peer_slow(b, parity, abort, limit);
     else return px_wait(b, parity, abort, limit);
 }
 __device__ __forceinline__ bool px_elect() {
@@ -475,7 +477,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
             const PxTile tl = tile_at(t, j);
             const int N = __shfl_sync(0xffffffffu, (tl.nvalid + 15) & ~15, 0);
             const int buf = j & 1;
-            ok = px_wait_all_tmem<PAIR>(&tempty[buf], (uint32_t(j >> 1) & 1u) ^ 1u, abort_flag, p.wait_ns);
+            ok = __all_sync(0xffffffffu, px_wait_peer<PAIR>(&tempty[buf], (uint32_t(j >> 1) & 1u) ^ 1u, abort_flag, p.wait_ns)) != 0;
             if (!ok) break;
             tc_fence_after();
             const uint32_t dacc = tmem + uint32_t(BN * buf);
@@ -488,8 +490,9 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
 #pragma unroll 4
                 for (int kb = 0; kb < nk; ++kb) {
                     if ((kb & (kPxChunk - 1)) == 0) {
-                        ok = px_wait_pair<PAIR>(&sfull[c % kPxSfBufs], uint32_t(c / kPxSfBufs) & 1u, abort_flag, p.wait_ns);
+                        ok = px_wait_peer<PAIR>(&sfull[c % kPxSfBufs], uint32_t(c / kPxSfBufs) & 1u, abort_flag, p.wait_ns);
                         if (!ok) break;
+                        if constexpr (PAIR) px_acquire_shared();
                     }
                     ok = px_wait(&full[st], ph, abort_flag, p.wait_ns);
                     if (!ok) break;
@@ -606,8 +609,12 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
-                if (PAIR && rank == 1) mbar_arrive_cluster(sfull_lead + 8u * b);
-                else mbar_arrive(&sfull[b]);
+                if (PAIR && rank == 1) {
+                    px_release_shared();
+                    px_arrive_peer(sfull_lead + 8u * b);
+                } else {
+                    mbar_arrive(&sfull[b]);
+                }
             }
             advance(2);
             load();
@@ -621,7 +628,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
         const int duo = 2 * half + (q >> 1), et = 32 * (q & 1) + lane;      // pair 0..3, thread 0..63 of it
         const auto release = [&](int buf) {
             if (lane) return;
-            if constexpr (PAIR) px_release_tmem(tempty_lead + 8u * buf);
+            if constexpr (PAIR) px_arrive_peer(tempty_lead + 8u * buf);
             else mbar_arrive(&tempty[buf]);
         };
         bool ok = true;
