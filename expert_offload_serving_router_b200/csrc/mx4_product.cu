@@ -203,14 +203,16 @@ __device__ __forceinline__ void px_ld_frag(uint32_t taddr, float (&v)[16]) {
 // paths: the E2M1 rounding that follows turns an error near a rounding border into a whole step.  The
 // exponent is carried in two floats (its rounding alone would cost |x| 2^-24), the reciprocal is
 // refined once.  2^88 and more divide to zero; the clamp keeps them out of inf * 0 in the refinement.
+// Flushing subnormals changes nothing: a subnormal exponent or power is lost in 1 + e, and d is in
+// 1 .. 2^121.
 __device__ __forceinline__ float px_silu(float x) {
     const float n = x * -1.44269502f;                                   // log2 e = 1.44269502 + 1.92596299e-8
     const float lo = fmaf(x, -1.44269502f, -n) - x * 1.92596299e-8f;
     float e;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(fminf(n, 120.f)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fminf(n, 120.f)));
     const float d = 1.f + fmaf(e, lo * 0.693147182f, e);
     float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(d));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
     r = fmaf(r, fmaf(-d, r, 1.f), r);
     return x * r;
 }
