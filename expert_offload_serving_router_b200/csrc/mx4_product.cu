@@ -14,13 +14,13 @@
 // is cut into ceil(n / BN) nearly equal pieces.  The tile list is built by every CTA from the group
 // offsets (a block scan), so nothing but the offsets has to come from the caller.
 //   BN = 32:   decode batches: 8 stages of 20 KB keep 128 KB of weights in flight per SM.  Bound by HBM
-//              (256 groups, 12 rows each, 4096 x 4096: 361 us, 6.3 TB/s).
-//   BN = 96:   a few dozen rows a group: 6 stages of 28 KB (48 rows each: 394 us, 5.9 TB/s).
+//              (256 groups, 12 rows each, 4096 x 4096: 345 us, 6.7 TB/s).
+//   BN = 96:   a few dozen rows a group: 6 stages of 28 KB (256 groups, 48 rows each, 2048 x 4096: 190 us, 6.4 TB/s).
 //   BN = 224:  long prompts, on CTA pairs (cta_group::2, M = 256): each CTA loads 128 weight rows and half
 //              of the tile's rows of `a`, 5 stages of 30 KB; two accumulators of 224 columns and two sets
 //              of scale columns fill the 512 TMEM columns.  One CTA per tile moves 40 KB per 256-deep
-//              stage and SM and ran at 580-600 us where pairs take 550 (256 groups x 192 rows, 4096 x 4096:
-//              2.8 GB, 1.65 PFLOP; clocks fall to ~1.4 GHz under the power cap).
+//              stage and SM and ran at 580-600 us where pairs took 550 and now take 508-580 (256 groups x 192
+//              rows, 4096 x 4096: 2.8 GB, 1.65 PFLOP; clocks fall to ~1.4 GHz under the power cap).
 //
 // Roles of the persistent CTA: warp 0 TMA producer (codes of both operands, 256-deep K stages, 128-byte
 // swizzle); warp 1 TMEM allocator and MMA issuer; warps 2-9 read the row-major scale bytes and lay them
@@ -28,7 +28,8 @@
 // 4 (row / 32) + j = row's scale of the step's block j); warps 10-17 epilogue, two per TMEM lane quarter.
 // The MMA warp copies a stage's atoms into TMEM right before the stage's MMAs (copies and MMAs of one
 // thread complete in issue order).  Alone on an SM a stage of N = 192 costs 417 clocks (the MMAs 384,
-// the six copies hide behind them); beside the other roles it is about twice that.
+// the six copies hide behind them).  Beside the other roles the issuing lane spends 380 a stage on
+// copies, MMAs and commits -- the four schedulers' other warps run other code -- and waits up to 280 for data.
 // Every wait is bounded.
 #include "decode_common.cuh"
 #include "gemm_common.cuh"
@@ -464,10 +465,12 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------ scale copies and MMAs
-        // The whole warp runs the loop and one elected lane issues: with warp-uniform control flow the
-        // descriptors stay in uniform registers, where the tcgen05 instructions want them.  (Under
-        // `if (lane == 0)` every operand is moved there one by one: 1200 clocks a stage of N = 192
-        // against under 800.)
+        // One elected lane runs a tile's K loop: under elect.sync the descriptors stay in uniform registers,
+        // where the tcgen05 instructions want them.  (Under `if (lane == 0)` every operand is moved there
+        // one by one: 1200 clocks a stage of N = 192 against under 800 then; the whole warp looping and the
+        // elected lane issuing paid a vote and a reconvergence a stage.)  The loop is unrolled by a chunk,
+        // so that scale columns and atom offsets are constants: per stage 550 clocks of issue became 370
+        // (one token, 6 of 256 groups, 4096 x 4096: 18.1 -> 16.6 us).
         const int utotal = rank == 0 ? __shfl_sync(0xffffffffu, total, 0) : 0;      // the leader issues for the pair
         const bool leader = px_elect();
         const uint64_t ad0 = sdesc_sw128(su32(sA)), bd0 = sdesc_sw128(su32(sB));
@@ -800,12 +803,12 @@ static int launch_variant(int64_t tiles, cudaStream_t st, const CUtensorMap& tw,
 
 // Which tile: the persistent workers (CTAs, or pairs) take rounds of tiles, so the estimate is rounds
 // times the measured time of a round, 6.5 : 8 : 12 for the three tiles (K = 4096, one round of each:
-// 9.9, 11.2 and 14.7 us).  Row tiles of a group: one while its average is well inside the tile, else as
-// many as the bound allows.  Measured (us, BN = 32 / 96 / pairs; the pick is the smallest but for the
-// first, where all three are within 7 %):
-//   256 groups x 24 rows, 4096 x 4096: 386 / 379 / 406;   x 48: 691 / 404 / 425;   x 192: - / - / 550
-//   129 groups x 143 rows, 1408 x 2816: 189 / 93 / 71;    one group, 4096 x 4096: 64 rows 9.9 / 10.3 / 12.7,
-//   200 rows 16.2 / 11.2 / 14.7, 800 rows 40 / 18 / 16;   1000 rows, 256 x 4096: 9.9 / 11.6 / 14.5
+// 8.7, 10.1 and 13.8 us).  Row tiles of a group: one while its average is well inside the tile, else as
+// many as the bound allows.  Measured (us, BN = 32 / 96 / pairs; the pick is the smallest of each):
+//   256 groups, 2048 x 4096: 8 rows each 177 / 179 / 189, 24 183 / 184 / 194, 32 206 / 186 / 196, 97 494 / 262 / 218;
+//   128 groups, 2816 x 704: 8 rows 27.8 / 29.2 / 31.3, 32 38.7 / 30.0 / 32.6, 128 111 / 55 / 42;   one group, 4096 x 4096:
+//   64 rows 8.7 / 8.9 / 10.4, 200 13.4 / 10.3 / 13.8, 400 18.6 / 15.9 / 14.0, 1600 58 / 28 / 21;   1000 rows, 512 x 4096:
+//   8.7 / 10.1 / 13.8.
 static int pick_tile(const Mx4Launch& L, int row_groups) {
     const double groups = L.G < L.R ? L.G : L.R, avg = L.R / groups;
     const int bn[3] = {32, 96, 224};
