@@ -200,22 +200,42 @@ __device__ __forceinline__ void px_ld_frag(uint32_t taddr, float (&v)[16]) {
         : "r"(taddr));
 }
 
-// silu(x) = x / (1 + 2^(-x log2 e)) to a few fp32 roundings -- not the tanh approximation of the bf16
-// paths: the E2M1 rounding that follows turns an error near a rounding border into a whole step.  The
-// exponent is carried in two floats (its rounding alone would cost |x| 2^-24), the reciprocal is
-// refined once.  2^88 and more divide to zero; the clamp keeps them out of inf * 0 in the refinement.
-// Flushing subnormals changes nothing: a subnormal exponent or power is lost in 1 + e, and d is in
-// 1 .. 2^121.
+// silu(x) = x / (1 + 2^(-x log2 e)) to a few fp32 roundings for |x| < kPxNear -- not the tanh approximation
+// of the bf16 paths: the E2M1 rounding that follows turns an error near a rounding border into a whole step.
+// The exponent is carried in two floats (its rounding alone would cost |x| 2^-24), the reciprocal takes one
+// Newton step.  The power is below 2^116, so nothing overflows, and flushing subnormals changes nothing: a
+// subnormal exponent or power is lost in 1 + e.  NaN stays NaN.
+constexpr float kPxNear = 80.f;
 __device__ __forceinline__ float px_silu(float x) {
     const float n = x * -1.44269502f;                                   // log2 e = 1.44269502 + 1.92596299e-8
     const float lo = fmaf(x, -1.44269502f, -n) - x * 1.92596299e-8f;
     float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fminf(n, 120.f)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(n));
     const float d = 1.f + fmaf(e, lo * 0.693147182f, e);
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
     r = fmaf(r, fmaf(-d, r, 1.f), r);
     return x * r;
+}
+// silu(x) * u for any x, as x u / (1 + z) for x >= 0 and x z u / (1 + z) for x < 0 with z = e^-|x| <= 1, so that
+// nothing overflows.  Below -kPxNear, z is kept as 2^126 z and 2^-126 multiplies u instead: a large u still
+// meets it, and what then flushes (|x| > 174) is below 2^-116 whatever u is.  |x| is bounded at 190, where z u is
+// zero for any u: unbounded, the exponent and its low part would grow with |x| until they overflow.  NaN
+// stays NaN, +inf is inf, -inf NaN (-inf * 0), as in the formula.
+__device__ __forceinline__ float px_silu_far(float x, float u) {
+    const float c = fminf(fabsf(x), 190.f);
+    const bool far = x < -kPxNear;
+    const float n = c * -1.44269502f;
+    const float lo = fmaf(c, -1.92596299e-8f, fmaf(c, -1.44269502f, -n));
+    const float w = far ? 0x1p-126f : 1.f;
+    float z;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(z) : "f"(far ? n + 126.f : n));
+    z = fmaf(z, lo * 0.693147182f, z);
+    const float d = fmaf(z, w, 1.f);                                    // 1 .. 2
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+    r = fmaf(r, fmaf(-d, r, 1.f), r);
+    return x * r * (x < 0.f ? z : 1.f) * (u * w);
 }
 
 struct PxTile { int g, m, row0, nvalid; };
@@ -677,9 +697,19 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                     // place of the fragment.  h is staged as fp32 [token][32 f of the pair]
                     float* hb = reinterpret_cast<float*>(sEpi) + duo * 32 * kPxHRow;
                     float* hw = hb + (lane & 3) * 2 * kPxHRow + 16 * (q & 1) + (lane >> 2);
+                    const auto put = [&](int i, float h) { hw[(8 * (i >> 2) + (i & 1)) * kPxHRow + 8 * ((i >> 1) & 1)] = h; };
+                    // one look at the sixteen gates: the form for any gate everywhere costs 1 % (2049 tokens, 8 of
+                    // 128 + 1, 2816 x 704: 123.3 us, 122.1 with the short form where it holds)
+                    float top = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        hw[(8 * (i >> 2) + (i & 1)) * kPxHRow + 8 * ((i >> 1) & 1)] = px_silu(v0[i]) * v1[i];
+                    for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(v0[i]));
+                    if (__builtin_expect(top < kPxNear, 1)) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) put(i, px_silu(v0[i]) * v1[i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) put(i, px_silu_far(v0[i], v1[i]));
+                    }
                     px_bar(1 + duo);
                     const int tok = et >> 1, part = et & 1;   // two threads per 32-element block
                     const float4* hr = reinterpret_cast<const float4*>(hb + tok * kPxHRow + 16 * part);

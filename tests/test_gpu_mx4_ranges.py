@@ -1,0 +1,67 @@
+"""The MXFP4 product and experts at the ends of their ranges: gates from subnormal results of SiLU to the largest finite
+values."""
+import numpy as np
+import pytest
+
+import mx4_util as M
+from expert_offload_serving_router_b200 import ftmoe as F
+from test_gpu_mx4 import cuda, new_ws, q_interval
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from gpu_util import ensure_built
+    ensure_built()
+
+
+# per 32-element block of h: gates sign x {0.5 .. 6} x 2^e, all with up = 2^u
+GATES = [(s, e, u) for s, e, u in [
+    (-1, -3, 0), (1, -3, 0), (-1, 1, 0), (1, 1, 0), (-1, 4, 0), (1, 4, 0), (-1, 4, 100), (-1, 5, 120),
+    (-1, 7, 0), (1, 7, 0), (-1, 13, 0), (1, 13, 0), (-1, 13, 120), (-1, 20, 0), (1, 20, 0), (-1, 20, 120),
+    (-1, 27, 0), (-1, 30, 0), (-1, 31, 120), (-1, 33, 0), (1, 33, 0), (-1, 40, 0), (-1, 66, 120), (1, 66, 10),
+    (-1, 100, 0), (1, 100, 0), (-1, 125, 0), (-1, 125, 120), (1, 125, -10), (1, 123, 0), (-1, 6, 90), (1, 6, 90)]]
+
+
+@pytest.mark.parametrize("T", [1, 700, 4000])      # a tile of 32 rows, of 96, of a pair
+def test_experts_mx4_gates_of_every_size(T):
+    """x = (1, 0, ...) and one nonzero weight a row, so that every gate is exact; W2 = the identity, so that o is h's
+    MXFP4 form.  h = silu(gate) up to a few fp32 roundings, 2^-20, and what the kernel flushes: below 2^-116."""
+    import torch
+    E, k, nb = 1, 1, len(GATES)
+    Fd = 32 * nb
+    H = Fd
+    assert H % 128 == 0
+    mag = np.resize(np.array([1, 2, 3, 4, 5, 6, 7], np.uint8), 32)          # codes of 0.5 1 1.5 2 3 4 6
+    code13 = np.zeros((E, 2 * Fd, H), np.uint8)
+    sc13 = np.full((E, 2 * Fd, H // 32), 127, np.uint8)
+    gate, up = np.zeros(Fd), np.zeros(Fd)
+    for b, (s, e, u) in enumerate(GATES):
+        f = slice(32 * b, 32 * b + 32)
+        code13[0, f, 0] = mag | (8 if s < 0 else 0)
+        code13[0, Fd + 32 * b:Fd + 32 * b + 32, 0] = 2
+        sc13[0, f, 0] = 127 + e
+        sc13[0, Fd + 32 * b:Fd + 32 * b + 32, 0] = 127 + u
+        gate[f] = s * M.GRID[mag] * 2.0 ** e
+        up[f] = 2.0 ** u
+    code2 = np.zeros((E, H, Fd), np.uint8)
+    code2[0, np.arange(Fd), np.arange(Fd)] = 2
+    d = [cuda(a) for a in (M.pack(code13), sc13, M.pack(code2), np.full((E, H, Fd // 32), 127, np.uint8))]
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = 1
+    shape = F.make_shape(H, Fd, E, k, 0, F.FT_W_MXFP4)
+    ws = new_ws(F.ft_moe_workspace_bytes(shape, T))
+    o = torch.full((T, H), 3.0, dtype=torch.bfloat16, device="cuda")
+    off, inv = cuda(np.array([0, T], np.int32)), cuda(np.arange(T, dtype=np.int32))
+    F.ft_moe_experts_mx4(shape, T, F.make_weights(*d), x, off, inv, o, ws)
+    F.ft_moe_check(ws)
+    with np.errstate(over="ignore"):
+        h = (M.silu(gate) * up)[None]
+    assert np.abs(h).max() < 3.4e38
+    want, far = q_interval(h, 2.0 ** -20 * np.abs(h) + 2.0 ** -116)
+    assert (far[0] <= 2.0 ** -114).mean() > 0.9                             # hardly any value near a rounding border
+    got = o.double().cpu().numpy()
+    assert np.isfinite(got).all(), f"{(~np.isfinite(got)).sum()} of {got.size} are not finite"
+    bad = ~(np.abs(got - want) <= far + 2.0 ** -116)
+    assert not bad.any(), f"first at {np.argwhere(bad)[0]}: {got[bad][:4]}"
