@@ -25,14 +25,18 @@ namespace ftmoe {
 // the register budget is cut for (more warps in flight hide the load latency of small batches).
 template <int TB, bool MX, bool FULLX, int U, int MINB>
 __global__ void __launch_bounds__(256, MINB) decode_gateup_kernel(DecodeArgs a) {
-    // FULLX: every token row [T][H] staged once (bf16, or f16 for MXFP4) before the
-    // programmatic dependency wait -- the layer input is complete before the router ran --
-    // so the routing-dependent part starts straight with the weight stream.
+    // FULLX: every token row [T][H] staged once (bf16, or f16 for MXFP4).  Behind the router of a
+    // layer call that is done before the programmatic dependency wait -- the layer input is complete
+    // before the router starts its dependents -- so the routing-dependent part starts straight with
+    // the weight stream.  The experts called alone (no y) may follow any kernel, one that is still
+    // writing x among them, and wait first.
     extern __shared__ uint4 xs4[];
     __shared__ int stok[TB];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (FULLX)
+    if (FULLX) {
+        if (!a.y) pdl_wait();
         for (int t = warp; t < a.T; t += 8) stage_x_row<MX>(a, xs4, t, t, lane);
+    }
     pdl_wait();
     pdl_trigger();
     gateup_items<TB, MX, FULLX, U>(a, xs4, stok, blockIdx.x, gridDim.x);

@@ -65,3 +65,87 @@ def test_experts_mx4_gates_of_every_size(T):
     assert np.isfinite(got).all(), f"{(~np.isfinite(got)).sum()} of {got.size} are not finite"
     bad = ~(np.abs(got - want) <= far + 2.0 ** -116)
     assert not bad.any(), f"first at {np.argwhere(bad)[0]}: {got[bad][:4]}"
+
+
+# ------------------------------------------------------------------ one call behind another, no wait in between
+def _consumer(g, wdtype, T, H, Fd, E, k):
+    """ft_moe_experts on its GEMV path, with routing made beforehand: (x, call(o))."""
+    import torch
+    shape = F.make_shape(H, Fd, E, k, 0, wdtype)
+    ws = new_ws(F.ft_moe_workspace_bytes(shape, T))
+    if wdtype == F.FT_W_MXFP4:
+        q13, q2 = M.random_weights(g, E, 2 * Fd, H), M.random_weights(g, E, H, Fd)
+        d = [cuda(a) for a in (*q13, *q2)]
+        weights = F.make_weights(*d)
+    else:
+        d = [torch.from_numpy(g.standard_normal(s) * 0.05).to(torch.bfloat16).cuda() for s in ((E, 2 * Fd, H), (E, H, Fd))]
+        weights = F.make_weights(d[0], None, d[1], None)
+    idx = cuda(np.stack([g.choice(E, size=k, replace=False) for _ in range(T)]).astype(np.int32))
+    i32 = lambda n: torch.empty(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    off, sf, inv = i32(E + 1), i32(T * k), i32(T * k)
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    F.ft_moe_permute(shape, T, idx, None, off, sf, inv, None, ws)
+    F.ft_moe_check(ws)
+
+    def call(o):
+        F.ft_moe_experts(shape, T, weights, x, None, off, sf, o, ws)
+    call.keep = (d, off, sf, inv, ws)
+    return x, call
+
+
+def _producer(g, kind, T, H, x):
+    """A call that writes x [T, H] and lets the kernel behind it start before it is done."""
+    import torch
+    if kind == "product":
+        K = 8192
+        code, scale = M.quantize(g.standard_normal((T, K)))
+        wc, wsc = M.random_weights(g, 1, H, K, lo=115, hi=119)
+        a = [cuda(v) for v in (np.array([0, T], np.int32), M.pack(code), scale, wc, wsc)]
+        ws = new_ws()
+        return lambda: F.ft_mx4_product(1, T, H, K, *a, x, ws)
+    E, k, Fd = 16, 4, 1024
+    # x of a size that keeps the consumer's h inside the f16 range which MXFP4 GEMVs on bf16 activations document
+    d = [cuda(a) for a in (*M.random_weights(g, E, 2 * Fd, H, lo=115, hi=119), *M.random_weights(g, E, H, Fd, lo=115, hi=119))]
+    weights = F.make_weights(*d)
+    z = torch.from_numpy(g.standard_normal((T, H))).to(torch.bfloat16).cuda()
+    if kind == "experts_mx4":
+        shape = F.make_shape(H, Fd, E, 1, 0, F.FT_W_MXFP4)
+        ws = new_ws(F.ft_moe_workspace_bytes(shape, T))
+        off, inv = np.zeros(E + 1, np.int32), cuda(np.arange(T, dtype=np.int32))
+        off[1:] = T
+        off = cuda(off)
+        keep = (d, z, ws, off, inv)
+        return lambda: keep and F.ft_moe_experts_mx4(shape, T, weights, z, off, inv, x, ws)
+    shape = F.make_shape(H, Fd, E, k, 0, F.FT_W_MXFP4)
+    ws = new_ws(F.ft_moe_workspace_bytes(shape, T))
+    wr = torch.from_numpy(g.standard_normal((E, H)).astype(np.float32) * 0.02).cuda()
+    fn = {"layer": F.ft_moe_layer_forward, "layer_mx4": F.ft_moe_layer_forward_mx4}[kind]
+    keep = (d,)
+    return lambda: keep and fn(shape, T, z, wr, None, weights, x, None, None, ws)
+
+
+@pytest.mark.parametrize("kind", ["product", "experts_mx4", "layer", "layer_mx4"])
+@pytest.mark.parametrize("wdtype", [F.FT_W_BF16, F.FT_W_MXFP4])
+@pytest.mark.parametrize("T", [1, 3])
+def test_experts_read_what_the_call_before_them_wrote(T, wdtype, kind):
+    """ft_moe_experts on x straight behind the call that writes x: the same bits as with a wait in between, each time with
+    other contents in x before."""
+    import torch
+    g = np.random.default_rng(T + 10 * wdtype)
+    H, Fd, E, k = 2048, 512, 8, 2
+    x, experts = _consumer(g, wdtype, T, H, Fd, E, k)
+    produce = _producer(g, kind, T, H, x)
+    want = torch.empty(T * k, H, dtype=torch.bfloat16, device="cuda")
+    produce()
+    torch.cuda.synchronize()
+    experts(want)
+    torch.cuda.synchronize()
+    assert torch.isfinite(want.float()).all() and want.float().abs().max() > 0
+    outs = [torch.empty_like(want) for _ in range(20)]
+    for i, o in enumerate(outs):
+        x.fill_(float(i + 1))
+        produce()
+        experts(o)
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o.view(torch.int16), want.view(torch.int16))
