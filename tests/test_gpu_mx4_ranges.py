@@ -149,3 +149,86 @@ def test_experts_read_what_the_call_before_them_wrote(T, wdtype, kind):
     torch.cuda.synchronize()
     for o in outs:
         assert torch.equal(o.view(torch.int16), want.view(torch.int16))
+
+
+# ------------------------------------------------------------------ more tokens than a grid's second dimension holds
+def _check_combine(y, o, inv, gw, T, k, S):
+    """y against the 64-bit combine of the rows o: one bf16 rounding and k + S + 1 fp32 ones."""
+    for lo in range(0, T, 16384):
+        hi = min(T, lo + 16384)
+        terms = o[inv[lo * k:hi * k].long()].double().view(hi - lo, k, -1) * gw[lo:hi].double()[..., None]
+        want, mag = terms.sum(1), terms.abs().sum(1)
+        if S:
+            sh = o[inv[T * k + lo:T * k + hi].long()].double()
+            want, mag = want + sh, mag + sh.abs()
+        assert ((y[lo:hi].double() - want).abs() <= M.UB16 * want.abs() + 2 * (k + S + 1) * M.U32 * mag).all()
+
+
+@pytest.mark.parametrize("T,H,k,S", [(65535, 128, 2, 1), (65536, 128, 2, 1), (70001, 128, 3, 0), (65537, 2176, 2, 0)])
+def test_combine_beyond_65535_tokens(T, H, k, S):
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    R = T * (k + S)
+    o = torch.randn(R, H, device="cuda", generator=gen).to(torch.bfloat16)
+    inv = torch.randperm(R, device="cuda", generator=gen).to(torch.int32)
+    gw = torch.rand(T, k, device="cuda", generator=gen)
+    y = torch.full((T + 1, H), 3.0, dtype=torch.bfloat16, device="cuda")
+    F.ft_moe_combine(F.make_shape(H, 64, 8, k, S), T, o, inv, gw, y)
+    torch.cuda.synchronize()
+    assert (y[T] == 3.0).all()
+    _check_combine(y[:T], o, inv, gw, T, k, S)
+
+
+@pytest.mark.parametrize("T,S", [(65536, 1), (66001, 0)])
+def test_layer_forward_mx4_beyond_65535_tokens(T, S):
+    """The layer call = its steps bit for bit, and the combine of their rows in 64 bits."""
+    import torch
+    g = np.random.default_rng(T)
+    H, Fd, E, k = 128, 64, 8, 2
+    d = [cuda(a) for a in (*M.random_weights(g, E, 2 * Fd, H), *M.random_weights(g, E, H, Fd))]
+    sh = [cuda(a) for a in (*M.random_weights(g, 1, 2 * Fd, H), *M.random_weights(g, 1, H, Fd))] if S else []
+    weights = F.make_weights(*d, None, *sh)
+    x = torch.from_numpy(g.standard_normal((T, H))).to(torch.bfloat16).cuda()
+    wr = torch.from_numpy(g.standard_normal((E, H)).astype(np.float32) * 0.1).cuda()
+    shape = F.make_shape(H, Fd, E, k, S, F.FT_W_MXFP4)
+    R = T * (k + S)
+    ws = new_ws(F.ft_moe_workspace_bytes(shape, T))
+    y = torch.full((T + 1, H), 3.0, dtype=torch.bfloat16, device="cuda")
+    F.ft_moe_layer_forward_mx4(shape, T, x, wr, None, weights, y, None, None, ws)
+    F.ft_moe_check(ws)
+    assert (y[T] == 3.0).all()
+    i32 = lambda *s: torch.empty(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    idx, gw, off, sf, inv = i32(T, k), torch.empty(T, k, device="cuda"), i32(E + S + 1), i32(R), i32(R)
+    o, y2 = torch.empty(R, H, dtype=torch.bfloat16, device="cuda"), torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    F.ft_moe_route(shape, T, x, wr, None, idx, gw, None, ws)
+    F.ft_moe_permute(shape, T, idx, None, off, sf, inv, None, ws)
+    F.ft_moe_experts_mx4(shape, T, weights, x, off, inv, o, ws)
+    F.ft_moe_combine(shape, T, o, inv, gw, y2)
+    F.ft_moe_check(ws)
+    assert torch.equal(y[:T].view(torch.int16), y2.view(torch.int16))
+    _check_combine(y[:T], o, inv, gw, T, k, S)
+
+
+def test_layer_forward_beyond_65535_tokens():
+    """The bf16 layer on the same grid: its last tokens equal the same tokens in a call of their own, up to the order in
+    which the router's K splits are added (their number goes by T)."""
+    import torch
+    g = np.random.default_rng(5)
+    T, H, Fd, E, k = 65600, 128, 64, 8, 2
+    d = [torch.from_numpy(g.standard_normal(s) * 0.1).to(torch.bfloat16).cuda() for s in ((E, 2 * Fd, H), (E, H, Fd))]
+    weights = F.make_weights(d[0], None, d[1], None)
+    x = torch.from_numpy(g.standard_normal((T, H))).to(torch.bfloat16).cuda()
+    wr = torch.from_numpy(g.standard_normal((E, H)).astype(np.float32) * 0.1).cuda()
+    shape = F.make_shape(H, Fd, E, k)
+    ws = new_ws(F.ft_moe_workspace_bytes(shape, T))
+    y, few = torch.empty(T, H, dtype=torch.bfloat16, device="cuda"), torch.empty(1000, H, dtype=torch.bfloat16, device="cuda")
+    idx, idx2 = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(1000, k, dtype=torch.int32, device="cuda")
+    F.ft_moe_layer_forward(shape, T, x, wr, None, weights, y, idx, None, ws)
+    F.ft_moe_check(ws)
+    F.ft_moe_layer_forward(shape, 1000, x[-1000:], wr, None, weights, few, idx2, None, ws)
+    F.ft_moe_check(ws)
+    same = (idx[-1000:] == idx2).all(1)
+    assert same.float().mean() > 0.99                                # two logits may swap within their last bits
+    diff = (y[-1000:].float() - few.float()).abs()[same]
+    # gates a few fp32 roundings apart: at most a neighbouring bf16 value
+    assert (diff <= 2 * M.UB16 * torch.maximum(y[-1000:].float().abs(), few.float().abs())[same] + 1e-6).all()
