@@ -75,6 +75,7 @@ ft_status check_ws(const ft_moe_shape* s, int T, const void* ws, size_t ws_bytes
 
 ft_status cuda_ok(cudaError_t e, const char* what) {
     if (e == cudaSuccess) return FT_OK;
+    cudaGetLastError();     // reported here: unless it is sticky, the next call must not fail with it too
     return fail(FT_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 

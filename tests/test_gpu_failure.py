@@ -51,3 +51,26 @@ def test_pipeline_wait_timeout_is_reported_and_the_next_call_is_exact(name, T, k
     assert np.array_equal(y2, y_ref), "the call after the timed-out one differs"
     torch.cuda.synchronize()
     assert host(y, np.uint16).shape == (T, cfg.hidden)
+
+
+def test_an_error_is_reported_once():
+    """A call that the runtime refuses (a synchronisation of a capturing stream: refused on the host, nothing runs)
+    reports it; the calls after it do not report it again."""
+    import ctypes
+    import torch
+    cu = ctypes.CDLL("libcuda.so.1")
+    ws = torch.empty(4096, dtype=torch.uint8, device="cuda")
+    F.ft_moe_workspace_init(ws)
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = ctypes.c_void_p()
+    assert cu.cuStreamBeginCapture_v2(ctypes.c_void_p(st.cuda_stream), 2) == 0     # relaxed
+    try:
+        with pytest.raises(F.FtError) as ei:
+            F.ft_moe_check(ws, stream=st)
+    finally:
+        assert cu.cuStreamEndCapture(ctypes.c_void_p(st.cuda_stream), ctypes.byref(graph)) != 0   # the capture was broken off
+    assert ei.value.status == F.FT_ERR_CUDA
+    F.ft_moe_workspace_init(ws)
+    F.ft_moe_check(ws)
+    F.ft_moe_check(ws, stream=st)
