@@ -176,6 +176,16 @@ def _here(*tensors):
             raise FtError(FT_ERR_INVALID_ARG, f"a tensor is on {t.device}, but device {dev} is current")
 
 
+def _weights_here(weights):
+    """The same for the tensors that make_weights was given (a field that was set to another address since is not theirs)."""
+    dev = None
+    for name, at, d in getattr(weights, "placed", ()):
+        if dev is None:
+            dev = (_torch or _load_torch()).cuda.current_device()
+        if d != dev and getattr(weights, name) == at:
+            raise FtError(FT_ERR_INVALID_ARG, f"{name} is on {'the host' if d < 0 else f'device {d}'}, but device {dev} is current")
+
+
 def _check(st: int):
     if st != FT_OK:
         raise FtError(st, lib().ft_last_error().decode())
@@ -194,8 +204,13 @@ def make_shape(hidden, ffn, num_experts, top_k, num_shared=0, wdtype=FT_W_BF16) 
 
 def make_weights(w13=None, w13_scale=None, w2=None, w2_scale=None, expert_ptrs=None, shared_w13=None,
                  shared_w13_scale=None, shared_w2=None, shared_w2_scale=None) -> ft_moe_weights:
-    return ft_moe_weights(_p(w13), _p(w13_scale), _p(w2), _p(w2_scale), _p(expert_ptrs), _p(shared_w13),
-                          _p(shared_w13_scale), _p(shared_w2), _p(shared_w2_scale))
+    given = (w13, w13_scale, w2, w2_scale, expert_ptrs, shared_w13, shared_w13_scale, shared_w2, shared_w2_scale)
+    at = [_p(t) for t in given]
+    w = ft_moe_weights(*at)
+    # where the tensors among them live, for the calls that check it (the struct itself holds addresses only)
+    w.placed = [(name, p, t.get_device()) for (name, _), p, t in zip(ft_moe_weights._fields_, at, given)
+                if hasattr(t, "get_device")]
+    return w
 
 
 # ---------------------------------------------------------------- entry points
@@ -310,6 +325,7 @@ def ft_mx4_product(groups, rows, n, k, offsets, a_codes, a_scales, w_codes, w_sc
 
 def ft_moe_experts_mx4(shape, T, weights, x, offsets, inv_pos, o_sorted, ws, ws_bytes=None, stream=None):
     _here(x, offsets, inv_pos, o_sorted, ws)
+    _weights_here(weights)
     _check(lib().ft_moe_experts_mx4(ctypes.byref(shape), T, ctypes.byref(weights), _p(x), _p(offsets), _p(inv_pos),
                                     _p(o_sorted), _p(ws), _nbytes(ws, ws_bytes), _s(stream)))
 
@@ -317,6 +333,7 @@ def ft_moe_experts_mx4(shape, T, weights, x, offsets, inv_pos, o_sorted, ws, ws_
 def ft_moe_layer_forward_mx4(shape, T, x, w_router, bias, weights, y, topk_idx_out, logits_out, ws, ws_bytes=None,
                              stream=None):
     _here(x, w_router, bias, y, topk_idx_out, logits_out, ws)
+    _weights_here(weights)
     _check(lib().ft_moe_layer_forward_mx4(ctypes.byref(shape), T, _p(x), _p(w_router), _p(bias), ctypes.byref(weights),
                                           _p(y), _p(topk_idx_out), _p(logits_out), _p(ws), _nbytes(ws, ws_bytes),
                                           _s(stream)))

@@ -171,3 +171,23 @@ def test_tensors_of_another_device_are_refused(monkeypatch, where):
     ]
     for fn, args in calls:
         assert "current" in refused(F.FT_ERR_INVALID_ARG, fn, *args)
+
+
+@pytest.mark.parametrize("where", [1, -1])
+@pytest.mark.parametrize("field", [0, 1, 2, 3, 5, 6, 7, 8])
+def test_weights_on_another_device_are_refused(monkeypatch, where, field):
+    import torch
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    here = _Elsewhere(0)
+    given = [here] * 4 + [None] + [here] * 4
+    given[field] = _Elsewhere(where)
+    w = F.make_weights(*given)
+    mx = F.make_shape(256, 128, 8, 2, 1, F.FT_W_MXFP4)
+    name = F.ft_moe_weights._fields_[field][0]
+    for fn, args in ((F.ft_moe_experts_mx4, (mx, 4, w, here, here, here, here, here, BIG)),
+                     (F.ft_moe_layer_forward_mx4, (mx, 4, here, here, None, w, here, None, None, here, BIG))):
+        msg = refused(F.FT_ERR_INVALID_ARG, fn, *args)
+        assert "current" in msg and name in msg
+    # an address put in its place is the caller's own, as everywhere; the calls go on to their other checks
+    setattr(w, name, FAKE + 1)
+    assert "current" not in refused(F.FT_ERR_INVALID_ARG, F.ft_moe_experts_mx4, mx, 4, w, here, here, here, here, here, BIG)
