@@ -91,6 +91,10 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(int T, int H, int
                 if (ps >= 0) *reinterpret_cast<uint4*>(d_o + int64_t(ps) * H + c * 8) = du;
             }
         }
+        // a dropped pair's product with zeros is NaN where dy is not finite
+#pragma unroll
+        for (int j = 0; j < KB; ++j)
+            if (pos[j] < 0) dot[j] = 0.f;
     }
     if (!d_w) return;
     tr_step(dot, 8, 16, lane);

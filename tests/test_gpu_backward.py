@@ -403,3 +403,19 @@ def test_routing_arrays_off_their_alignment(k):
     dx2 = permute_backward(s, dxs, moved(dl), wr)
     assert torch.equal(d_o.view(torch.int16), d_o2.view(torch.int16)) and torch.equal(d_w, d_w2)
     assert torch.equal(dx.view(torch.int16), dx2.view(torch.int16))
+
+
+@pytest.mark.parametrize("T,H,k", [(6, 256, 2), (300, 512, 4), (2000, 256, 3), (1100, 1280, 5)])     # 8, 4, 1 and 8 warps a token
+def test_dropped_pair_has_no_gradient_where_dy_is_not_finite(T, H, k):
+    import torch
+    s = setup(T, H, 8, k, 1)
+    dy, o = normal(s, T, H), normal(s, s["R"], H)
+    dy[2, 5], dy[3, 7], dy[4, 11] = float("inf"), float("nan"), float("-inf")
+    for t in (2, 3, 4, 5):
+        s["inv"][t * k + 1] = -1
+    _, d_w = combine_backward(s, dy, o)
+    _, only = combine_backward(s, dy, o, want_o=False)
+    assert torch.equal(d_w.view(torch.int32), only.view(torch.int32))
+    assert (d_w[2:6, 1] == 0).all()
+    assert not torch.isfinite(d_w[2:5, 0]).any()
+    assert torch.isfinite(d_w[5:]).all() and torch.isfinite(d_w[:2]).all()
