@@ -308,13 +308,7 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t st) {
     while (!fullx && TB > 1 && size_t(TB) * a.H * 2 > 65536) TB >>= 1;
     const size_t smem = size_t(fullx ? a.T : TB) * a.H * 2;
     int items = na_max * ((a.F + kFPB - 1) / kFPB);   // upper bound; the kernel strides over the real count
-    static int sms = 0;
-    if (!sms) {
-        int dev = 0;
-        cudaGetDevice(&dev);
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        if (sms <= 0) sms = 148;
-    }
+    const int sms = num_sms();
     // one-token batches: four (MXFP4: three) resident CTAs per SM, fewer vectors in flight per lane
     const bool wide = TB == 1 && fullx;
     const int per_sm = wide ? (mx ? 3 : 4) : 2;

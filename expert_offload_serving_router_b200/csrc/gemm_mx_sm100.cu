@@ -406,12 +406,12 @@ int launch_moe_gemm_mx_pair(const GemmLaunch& L, const GemmParams& p0, cudaStrea
         if (!make_map(&tb[i], L.act, 2, dims, str, box)) return 1;
     }
     constexpr size_t smem = mx_pair_smem_bytes();
-    static int max_clusters = 0;
     static PerDeviceOnce attr;
     if (attr([&] { return cudaFuncSetAttribute(moe_gemm_mx_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)); }) !=
         cudaSuccess)
         return 2;
-    if (!max_clusters) {   // the same on every device of one model: queried once
+    static PerDeviceCount max_clusters;
+    int clusters = max_clusters([&] {
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(2 * (num_sms() / 2));
         cfg.blockDim = dim3(kMxThreads);
@@ -421,9 +421,8 @@ int launch_moe_gemm_mx_pair(const GemmLaunch& L, const GemmParams& p0, cudaStrea
             cudaGetLastError();
             n = num_sms() / 2;
         }
-        max_clusters = n;
-    }
-    int clusters = max_clusters;
+        return n;
+    });
     const int pair_tiles = L.max_tiles * p.m_tiles;
     if (pair_tiles < clusters) clusters = pair_tiles > 0 ? pair_tiles : 1;
     moe_gemm_mx_pair_kernel<<<2 * clusters, kMxThreads, smem, st>>>(mc, ms, msc, mss, tb[0], tb[1], tb[2], tb[3], tb[4], p);

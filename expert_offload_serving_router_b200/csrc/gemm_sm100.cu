@@ -529,13 +529,13 @@ static int launch_pair(const GemmLaunch& L, const GemmParams& p, const CUtensorM
         uint32_t box[2] = {kBK, uint32_t(pp.b_rows[i])};
         if (!make_map(&tbp[i], L.act, 2, dims, str, box)) return 1;
     }
-    static int max_clusters = 0;
     constexpr size_t smem = C::smem();
     static PerDeviceOnce attr;
     if (attr([&] { return cudaFuncSetAttribute(moe_gemm_pair_kernel<HPC>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)); }) !=
         cudaSuccess)
         return 2;
-    if (!max_clusters) {   // the same on every device of one model: queried once
+    static PerDeviceCount max_clusters;
+    int clusters = max_clusters([&] {
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(2 * (num_sms() / 2));
         cfg.blockDim = dim3(320);
@@ -545,9 +545,8 @@ static int launch_pair(const GemmLaunch& L, const GemmParams& p, const CUtensorM
             cudaGetLastError();
             n = num_sms() / 2;
         }
-        max_clusters = n;
-    }
-    int clusters = max_clusters;
+        return n;
+    });
     const int pair_tiles = L.max_tiles * pp.m_tiles;
     if (pair_tiles < clusters) clusters = pair_tiles > 0 ? pair_tiles : 1;
     moe_gemm_pair_kernel<HPC><<<2 * clusters, 320, smem, st>>>(tw, tsw, tbp[0], tbp[1], tbp[2], tbp[3], tbp[4], pp);

@@ -808,17 +808,16 @@ static int launch_variant(int64_t tiles, cudaStream_t st, const CUtensorMap& tw,
     cfg.attrs = at;
     int workers = num_sms();       // persistent CTAs, or pairs: as many as fit at once
     if (PAIR) {
-        static int max_clusters = 0;   // the same on every device of one model: queried once
-        if (!max_clusters) {
+        static PerDeviceCount max_clusters;
+        workers = max_clusters([&] {
             cfg.gridDim = dim3(2 * (num_sms() / 2));
             int n = 0;
             if (cudaOccupancyMaxActiveClusters(&n, mx4_product_kernel<SWIGLU, BN, PAIR>, &cfg) != cudaSuccess || n <= 0) {
                 cudaGetLastError();
                 n = num_sms() / 2;
             }
-            max_clusters = n;
-        }
-        workers = max_clusters;
+            return n;
+        });
     }
     if (tiles < workers) workers = int(tiles);
     cfg.gridDim = dim3(PAIR ? 2 * workers : workers);
@@ -843,11 +842,12 @@ static int pick_tile(const Mx4Launch& L, int row_groups) {
     const double groups = L.G < L.R ? L.G : L.R, avg = L.R / groups;
     const int bn[3] = {32, 96, 224};
     const double cost[3] = {6.5, 8., 12.};
+    const int sms = num_sms();
     int best = 0;
     double least = 0.;
     for (int i = 0; i < 3; ++i) {
         const double tiles = groups * (avg <= 0.8 * bn[i] ? 1. : 1. + avg / bn[i]) * (i == 2 ? (row_groups + 1) / 2 : row_groups);
-        const double t = cost[i] * ceil(tiles / (i == 2 ? num_sms() / 2 : num_sms()));
+        const double t = cost[i] * ceil(tiles / (i == 2 ? sms / 2 : sms));
         if (i == 0 || t < least) { best = i; least = t; }
     }
     return best;

@@ -4,6 +4,7 @@
 #pragma once
 #include <cuda.h>
 #include "kernels.h"
+#include "per_device.h"
 
 namespace ftmoe {
 
@@ -220,24 +221,6 @@ inline bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t*
                      const uint32_t* box, CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B) {
     return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rank, dims, strides, box, sw);
 }
-int num_sms();
-
-// One-time setup per device: a kernel's cudaFuncSetAttribute values belong to the current
-// device's copy of it, so the flag is per device ordinal (devices past the table repeat the
-// setup on every call, which is correct, only slower).
-struct PerDeviceOnce {
-    static constexpr int kDevices = 64;
-    bool done[kDevices] = {};
-    template <typename Fn>
-    cudaError_t operator()(Fn&& fn) {
-        int d = -1;
-        if (cudaGetDevice(&d) != cudaSuccess) d = -1;
-        const bool slot = d >= 0 && d < kDevices;
-        if (slot && done[d]) return cudaSuccess;
-        const cudaError_t e = fn();
-        if (e == cudaSuccess && slot) done[d] = true;
-        return e;
-    }
-};
+int num_sms();      // of the current device
 
 }  // namespace ftmoe

@@ -35,14 +35,13 @@ bool make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank
 }
 
 int num_sms() {
-    static int n = 0;
-    if (!n) {
-        int dev = 0;
+    static PerDeviceCount count;
+    return count([] {
+        int dev = 0, n = 0;
         cudaGetDevice(&dev);
         cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-        if (n <= 0) n = 148;
-    }
-    return n;
+        return n > 0 ? n : 148;
+    });
 }
 
 }  // namespace ftmoe
