@@ -304,23 +304,25 @@ static cudaError_t permute_backward_go(int T, int H, int k, int S, int E, int R,
     // 8192 tokens: k = 5 (336 MB) 89 us without, 79 with; k = 8 (537 MB) 124 and 113; but 8192 x 2048, k = 8 and
     // a shared row (302 MB), 59.2 and 60.2, with E = 256 61 and 66.  Few rows a token: 70 and 64 (k = 4, 268 MB)
     // before the register bound above, 65 since.
-    if (wr && KB > 4 && (int64_t(k) + S) * T * H * 2 >= (320ll << 20)) {
-        // two waves of three CTAs an SM, not a CTA more (each reads its slice of W_r once)
-        const int slices = H / 64;
-        int64_t runs = 6 * num_sms() / slices > 0 ? 6 * num_sms() / slices : 1;
-        int64_t run = (T + runs - 1) / runs;
-        run = (run + kPbTokens - 1) / kPbTokens * kPbTokens;
-        runs = (T + run - 1) / run;
-        const size_t smem = size_t(E) * 256;
-        static PerDeviceOnce attr;
-        const cudaError_t e = attr([&] {
-            return cudaFuncSetAttribute(permute_backward_slice_kernel<KB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        kMaxExperts * 256);
-        });
-        if (e != cudaSuccess) return e;
-        permute_backward_slice_kernel<KB><<<dim3(slices, unsigned(runs)), kPbThreads, smem, st>>>(
-            T, H, k, S, E, R, int(run), dxs, inv_pos, idx, dl, wr, dx);
-        return cudaGetLastError();
+    if constexpr (KB > 4) {
+        if (wr && (int64_t(k) + S) * T * H * 2 >= (320ll << 20)) {
+            // two waves of three CTAs an SM, not a CTA more (each reads its slice of W_r once)
+            const int slices = H / 64;
+            int64_t runs = 6 * num_sms() / slices > 0 ? 6 * num_sms() / slices : 1;
+            int64_t run = (T + runs - 1) / runs;
+            run = (run + kPbTokens - 1) / kPbTokens * kPbTokens;
+            runs = (T + run - 1) / run;
+            const size_t smem = size_t(E) * 256;
+            static PerDeviceOnce attr;
+            const cudaError_t e = attr([&] {
+                return cudaFuncSetAttribute(permute_backward_slice_kernel<KB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            kMaxExperts * 256);
+            });
+            if (e != cudaSuccess) return e;
+            permute_backward_slice_kernel<KB><<<dim3(slices, unsigned(runs)), kPbThreads, smem, st>>>(
+                T, H, k, S, E, R, int(run), dxs, inv_pos, idx, dl, wr, dx);
+            return cudaGetLastError();
+        }
     }
     const int64_t blocks = (int64_t(T) * nv + 255) / 256;
     if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
