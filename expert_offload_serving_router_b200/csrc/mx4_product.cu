@@ -34,6 +34,7 @@
 #include "decode_common.cuh"
 #include "gemm_common.cuh"
 #include "mx4.cuh"
+#include "mx4_tiles.h"
 #include <cmath>
 
 namespace ftmoe {
@@ -238,28 +239,6 @@ __device__ __forceinline__ float px_silu_far(float x, float u) {
     return x * r * (x < 0.f ? z : 1.f) * (u * w);
 }
 
-struct PxTile { int g, m, row0, nvalid; };
-
-// tile t -> group, 128-row weight tile m (fastest, so CTAs that share rows of `a` run together), rows
-template <int BN>
-__device__ __forceinline__ PxTile px_tile(int t, const int* ntile, const int* off, int G, int m_tiles) {
-    PxTile r;
-    const int u = t / m_tiles;
-    r.m = t - u * m_tiles;
-    int lo = 0, hi = G;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (ntile[mid] <= u) lo = mid; else hi = mid;
-    }
-    r.g = lo;
-    const int n = off[lo + 1] - off[lo], nt = ntile[lo + 1] - ntile[lo];
-    const int per = ((n + nt - 1) / nt + 15) & ~15;     // <= BN, and (nt - 1) * per < n
-    const int i = u - ntile[lo];
-    r.row0 = off[lo] + i * per;
-    r.nvalid = min(per, n - i * per);
-    return r;
-}
-
 // 32 scale bytes (1024 elements) of a row, from byte 32 c on.  Bytes past the row's nsc are whatever
 // is there: the MMAs stop at K.  Rows that start off an 8-byte boundary (K / 32 not a multiple of 8)
 // are read as the aligned 8-byte words that hold them -- a word is read only if it holds a byte of the
@@ -335,7 +314,7 @@ mx4_product_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
         bad = lo < 0 || hi < lo || hi > p.R;
         off[tid] = lo;
         if (tid == G - 1) off[G] = hi;
-        nt = (hi - lo + BN - 1) / BN;
+        nt = px_row_tiles<BN>(hi - lo);      // a bad table's are dropped below
     }
     if (__syncthreads_or(bad)) {
         if (bad && blockIdx.x == 0) atomicExch(p.err, kDevErrOffsets);
