@@ -232,3 +232,38 @@ def test_layer_forward_beyond_65535_tokens():
     diff = (y[-1000:].float() - few.float()).abs()[same]
     # gates a few fp32 roundings apart: at most a neighbouring bf16 value
     assert (diff <= 2 * M.UB16 * torch.maximum(y[-1000:].float().abs(), few.float().abs())[same] + 1e-6).all()
+
+
+# ------------------------------------------------------------------ more tiles than a CTA works out ahead
+def _decode(codes, scales):
+    """Codes [..., cols / 2] and scale bytes [..., cols / 32] on the device -> fp64 values."""
+    import torch
+    grid = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64, device=codes.device)
+    grid = torch.cat([grid, -grid])
+    v = torch.stack([grid[(codes & 15).long()], grid[(codes >> 4).long()]], -1).flatten(-2)
+    return v * torch.exp2(scales.double() - 127).repeat_interleave(32, -1)
+
+
+# 148 CTAs (74 pairs) take 258 tiles each: 256 of them from the table, the others decoded in the roles' loops
+@pytest.mark.parametrize("sizes,n", [([1] * 256, 19072), ([60] * 256, 19072), ([10299, 10304, 10311], 35328)])
+def test_product_more_tiles_than_the_table(sizes, n):
+    import torch
+    k, G, rows = 64, len(sizes), sum(sizes)
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    byte = lambda *s, lo=0, hi=256: torch.randint(lo, hi, s, dtype=torch.uint8, device="cuda", generator=gen)  # noqa: E731
+    ac, asc = byte(rows, k // 2), byte(rows, k // 32, lo=120, hi=130)
+    wc, wsc = byte(G, n, k // 2), byte(G, n, k // 32, lo=119, hi=124)
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    out = torch.full((rows + 1, n), 3.0, dtype=torch.bfloat16, device="cuda")
+    ws = new_ws()
+    F.ft_mx4_product(G, rows, n, k, cuda(off), ac, asc, wc, wsc, out, ws)
+    F.ft_moe_check(ws)
+    assert (out[rows] == 3.0).all()
+    for g in range(G):
+        w = _decode(wc[g], wsc[g])
+        for lo in range(off[g], off[g + 1], 2048):
+            hi = min(off[g + 1], lo + 2048)
+            a = _decode(ac[lo:hi], asc[lo:hi])
+            want = a @ w.t()
+            tol = M.UB16 * want.abs() + M.sum_bound(k) * (a.abs() @ w.abs().t())
+            assert ((out[lo:hi].double() - want).abs() <= tol).all(), (g, lo)
