@@ -1,5 +1,6 @@
-"""The MXFP4 product and experts at the ends of their ranges: gates from subnormal results of SiLU to the largest finite
-values."""
+"""The MXFP4 calls at the ends of their ranges and behind other work: gates from subnormal results of SiLU to the largest
+finite values, more tokens and tiles than one grid or table holds, matrices past 2^31 elements, calls one behind another
+and captured behind other streams."""
 import numpy as np
 import pytest
 
@@ -267,3 +268,86 @@ def test_product_more_tiles_than_the_table(sizes, n):
             want = a @ w.t()
             tol = M.UB16 * want.abs() + M.sum_bound(k) * (a.abs() @ w.abs().t())
             assert ((out[lo:hi].double() - want).abs() <= tol).all(), (g, lo)
+
+
+def test_quantize_beyond_2_31_elements():
+    """The last rows of a matrix of 2.15e9 elements: as quantised on their own."""
+    import torch
+    rows, cols, n = 524800, 4096, 700
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x[:n].normal_(generator=torch.Generator(device="cuda").manual_seed(1))
+    for lo in range(n, rows, n):
+        x[lo:lo + n] = x[:min(n, rows - lo)]
+    x[-n:] *= 3
+    codes = torch.empty(rows, cols // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(rows, cols // 32, dtype=torch.uint8, device="cuda")
+    vals = torch.empty_like(x)
+    F.ft_mx4_quantize(rows, cols, F.FT_T_BF16, x, cols, codes, scales, vals)
+    for at in (0, rows // 2, rows - n):
+        c, s, v = torch.empty_like(codes[:n]), torch.empty_like(scales[:n]), torch.empty_like(vals[:n])
+        F.ft_mx4_quantize(n, cols, F.FT_T_BF16, x[at:at + n], cols, c, s, v)
+        assert torch.equal(c, codes[at:at + n]) and torch.equal(s, scales[at:at + n]) and torch.equal(v, vals[at:at + n])
+
+
+@pytest.mark.parametrize("rows", [40, 3000])
+@pytest.mark.parametrize("before", ["nothing", "memset", "another stream", "memset and another stream"])
+def test_calls_captured_behind_other_work(before, rows):
+    """The MXFP4 calls as programmatic dependents of what a capture may hold before them: the same bits as eagerly."""
+    import torch
+    g = np.random.default_rng(rows)
+    H, Fd, E, k = 256, 128, 4, 2
+    T = rows // 2
+    d = [cuda(a) for a in (*M.random_weights(g, E, 2 * Fd, H), *M.random_weights(g, E, H, Fd))]
+    weights = F.make_weights(*d)
+    shape = F.make_shape(H, Fd, E, k, 0, F.FT_W_MXFP4)
+    ws = new_ws(F.ft_moe_workspace_bytes(shape, T))
+    src = torch.from_numpy(g.standard_normal((T, H))).to(torch.bfloat16).cuda()
+    x = torch.zeros_like(src)
+    idx = np.stack([g.choice(E, size=k, replace=False) for _ in range(T)]).astype(np.int32)
+    i32 = lambda n: torch.empty(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    off, sf, inv = i32(E + 1), i32(T * k), i32(T * k)
+    F.ft_moe_permute(shape, T, cuda(idx), None, off, sf, inv, None, ws)
+    o = torch.empty(T * k, H, dtype=torch.bfloat16, device="cuda")
+    wr = torch.from_numpy(g.standard_normal((E, H)).astype(np.float32)).cuda()
+    y = torch.empty_like(src)
+    ac, asc = cuda(M.random_weights(g, rows, H)[0]), cuda(M.random_weights(g, rows, H)[1])
+    out = torch.empty(rows, 2 * Fd, dtype=torch.bfloat16, device="cuda")
+    goff = cuda(np.array([0, rows // 3, rows // 3, rows - 1, rows], np.int32))
+    pad = torch.ones(1 << 20, device="cuda")
+    ws_p = new_ws()
+    calls = [
+        lambda: F.ft_moe_experts_mx4(shape, T, weights, x, off, inv, o, ws),
+        lambda: F.ft_mx4_product(E, rows, 2 * Fd, H, goff, ac, asc, d[0], d[1], out, ws_p),
+        lambda: F.ft_moe_layer_forward_mx4(shape, T, x, wr, None, weights, y, None, None, ws),
+    ]
+    results = [o, out, y]
+    for call, res in zip(calls, results):
+        x.copy_(src)
+        call()
+        F.ft_moe_check(ws)
+        F.ft_moe_check(ws_p)
+        want = res.clone()
+        res.zero_()
+        x.zero_()
+        st, side = torch.cuda.Stream(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            if "stream" in before:
+                side.wait_stream(st)
+                with torch.cuda.stream(side):
+                    pad.mul_(1.0)
+                    x.copy_(src)
+            if "memset" in before:
+                pad.zero_()
+            if "stream" in before:
+                st.wait_stream(side)
+            call()
+        if "stream" not in before:
+            x.copy_(src)
+        for _ in range(2):
+            graph.replay()
+        torch.cuda.synchronize()
+        F.ft_moe_check(ws)
+        F.ft_moe_check(ws_p)
+        assert torch.equal(res.view(torch.int16), want.view(torch.int16))
