@@ -335,8 +335,9 @@ ft_status ft_moe_layer_forward_mx4(const ft_moe_shape* shape, int32_t T, const v
 /* ---------------------------------------------------------------------------
  * Gradients of steps 1, 2 and 4 (the experts' own gradient is the caller's).  Fixed-order fp32
  * sums, no atomics: the same inputs give the same bits.  inv_pos, offsets, sorted_flat: as
- * written by ft_moe_permute for topk_idx; a position outside [0,R) is a dropped pair (it
- * contributes nothing), and after a batch that ft_moe_check reported the results are undefined
+ * written by ft_moe_permute for topk_idx; a position outside [0,R) is a dropped pair (its row
+ * contributes nothing and its gate's gradient is zero; the router's terms go by topk_idx, dlogits
+ * and sorted_flat alone), and after a batch that ft_moe_check reported the results are undefined
  * but nothing out of range is touched.  T * (k + S) must fit in 31 bits.  Outputs must not
  * overlap inputs.
  * ------------------------------------------------------------------------- */

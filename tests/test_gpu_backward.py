@@ -419,3 +419,17 @@ def test_dropped_pair_has_no_gradient_where_dy_is_not_finite(T, H, k):
     assert (d_w[2:6, 1] == 0).all()
     assert not torch.isfinite(d_w[2:5, 0]).any()
     assert torch.isfinite(d_w[5:]).all() and torch.isfinite(d_w[:2]).all()
+
+
+def test_dropped_pair_keeps_the_routers_part():
+    """The router's part of dx goes by topk_idx and dlogits alone: a dropped pair's logit still moves the other gates."""
+    import torch
+    T, H, E, k = 6, 256, 4, 2
+    s = setup(T, H, E, k, 0)
+    dxs = normal(s, s["R"], H)
+    dl, wr = torch.randn(T, k, device="cuda"), torch.randn(E, H, device="cuda")
+    s["inv"][2 * k + 1] = -1
+    dx = permute_backward(s, dxs, dl, wr)
+    terms = torch.cat([dxs.double()[int(s["inv"][2 * k])][None], dl[2].double()[:, None] * wr.double()[s["idx"][2].long()]])
+    want, mag = terms.sum(0), terms.abs().sum(0)
+    assert ((dx[2].double() - want).abs() <= M.UB16 * want.abs() + 4 * M.U32 * (1 + M.UB16) * mag).all()
