@@ -19,8 +19,9 @@
 //   BN = 224:  long prompts, on CTA pairs (cta_group::2, M = 256): each CTA loads 128 weight rows and half
 //              of the tile's rows of `a`, 5 stages of 30 KB; two accumulators of 224 columns and two sets
 //              of scale columns fill the 512 TMEM columns.  One CTA per tile moves 40 KB per 256-deep
-//              stage and SM and ran at 580-600 us where pairs took 550 and now take 508-580 (256 groups x 192
-//              rows, 4096 x 4096: 2.8 GB, 1.65 PFLOP; clocks fall to ~1.4 GHz under the power cap).
+//              stage and SM and ran at 580-600 us where pairs took 550.  256 groups x 192 rows, 4096 x 4096
+//              (2.8 GB, 1.65 PFLOP): 510 us for calls a quarter of a second apart (a single launch ran at 1.50 GHz by
+//              its own cycle count), 635 us back to back, where the 1 kW power cap holds the SMs at 1.07 GHz.
 //
 // Roles of the persistent CTA: warp 0 TMA producer (codes of both operands, 256-deep K stages, 128-byte
 // swizzle); warp 1 TMEM allocator and MMA issuer; warps 2-9 read the row-major scale bytes and lay them
